@@ -183,7 +183,7 @@ static Ws layout(const Dims& d, bool bwd, const SplitPlan& sp) {
   return w;
 }
 
-static fix_status check_device() {
+fix_status check_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FIX_ERR_CUDA;
   int major = 0;
@@ -418,6 +418,7 @@ const char* fix_attn_status_string(int s) {
     case FIX_ERR_CUDA: return "FIX_ERR_CUDA: a CUDA call or kernel launch failed";
     case FIX_ERR_DEVICE_TIMEOUT: return "FIX_ERR_DEVICE_TIMEOUT: a bounded device wait expired";
     case FIX_ERR_ARCH: return "FIX_ERR_ARCH: the current device is not sm_100";
+    case FIX_ERR_PAGE: return "FIX_ERR_PAGE: a token has no page in the cache";
     default: return "unknown fix_status";
   }
 }

@@ -9,6 +9,10 @@ constexpr int ST_ROWS = 32;  // rows per CTA of the exact (SIMT) kernels
 
 // Validates a problem descriptor and fills the kernel-side dims (fix_api.cu).
 fix_status validate_problem(const fix_attn_problem* p, Dims* d);
+// FIX_OK if the current device is sm_100 (fix_api.cu).
+fix_status check_device();
+// Validates the sizes and pointers of a paged cache for `d` (fix_rotary.cu).
+fix_status validate_cache(const fix_attn_page_cache* c, const Dims& d);
 
 // Sizes of one decode call (fix_decode.cu).
 struct DecodeDims {

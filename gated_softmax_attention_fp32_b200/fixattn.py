@@ -20,7 +20,8 @@ from typing import Optional
 import torch
 
 __all__ = ["load", "Problem", "fix_attn_fwd", "fix_attn_bwd", "fix_attn_workspace_bytes",
-           "fix_attn_decode",
+           "fix_attn_decode", "fix_attn_rotary", "fix_rotary", "fix_attn_append_paged",
+           "fix_attn_decode_paged", "fix_attn_decode_paged_workspace",
            "fix_attn_device_status", "fix_attn", "training_workspace", "FixStatusError", "LIB_PATH",
            "EXPORTS"]
 
@@ -28,7 +29,9 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfixattn.
 EXPORTS = ("fix_attn_workspace_bytes", "fix_attn_fwd", "fix_attn_bwd", "fix_attn_device_status",
            "fix_attn_kernel_count", "fix_attn_status_string", "fix_attn_fwd_noalloc",
            "fix_attn_noalloc_device_status", "fix_attn_decode_workspace_bytes",
-           "fix_attn_decode")
+           "fix_attn_decode", "fix_attn_rotary", "fix_attn_append_paged",
+           "fix_attn_decode_paged_workspace_bytes", "fix_attn_decode_paged")
+FIX_ERR_PAGE = 12
 NOALLOC_MAX_WORKSPACE_BYTES = 16 * 1024 * 1024
 FIX_FLAG_REUSE_FWD_WORKSPACE = 1
 FIX_FLAG_NO_NORM = 2
@@ -49,6 +52,19 @@ class Problem(ctypes.Structure):
                 ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
                 ("scale", ctypes.c_float), ("eps", ctypes.c_float),
                 ("events", ctypes.c_void_p)]
+
+
+class Rotation(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class PageCache(ctypes.Structure):
+    _fields_ = [("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("page_table", ctypes.c_void_p),
+                ("seqlens", ctypes.c_void_p), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("g_pages", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
 
 
 class FixStatusError(RuntimeError):
@@ -84,6 +100,16 @@ def load():
     lib.fix_attn_decode_workspace_bytes.restype = sz
     lib.fix_attn_decode.argtypes = [P] + [vp] * 9 + [sz, vp]
     lib.fix_attn_decode.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    R, C = ctypes.POINTER(Rotation), ctypes.POINTER(PageCache)
+    lib.fix_attn_rotary.argtypes = [P, R, vp, vp, i64, vp, i64, vp, vp, ctypes.c_int, vp]
+    lib.fix_attn_rotary.restype = ctypes.c_int
+    lib.fix_attn_append_paged.argtypes = [P, C, R] + [vp, i64] * 4 + [vp, vp, vp]
+    lib.fix_attn_append_paged.restype = ctypes.c_int
+    lib.fix_attn_decode_paged_workspace_bytes.argtypes = [P, C]
+    lib.fix_attn_decode_paged_workspace_bytes.restype = sz
+    lib.fix_attn_decode_paged.argtypes = [P, C] + [vp] * 5 + [sz, vp]
+    lib.fix_attn_decode_paged.restype = ctypes.c_int
     lib.fix_attn_kernel_count.argtypes = [P, ctypes.c_int]
     lib.fix_attn_kernel_count.restype = ctypes.c_int
     lib.fix_attn_status_string.argtypes = [ctypes.c_int]
@@ -284,6 +310,290 @@ def fix_attn_decode(q, k_cache, v_cache, g_cache, seqlens, o_norm_weight=None, s
     return y
 
 
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(name, t, dtype, device):
+    """A tensor argument of the right type on the call's GPU."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _dense(name, t, dtype, device, shape):
+    _tensor(name, t, dtype, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _token_stride(name, t, inner):
+    """Elements between consecutive tokens of a [B,T,...] tensor whose inner
+    dims (``inner`` elements) are dense: a dense tensor or a slice of a fused
+    projection's output.  Anything else raises."""
+    if t.is_contiguous():
+        return inner
+    B, T, shape, st = t.shape[0], t.shape[1], t.shape, t.stride()
+    dense, run = True, 1
+    for i in range(t.dim() - 1, 1, -1):
+        dense = dense and (shape[i] == 1 or st[i] == run)
+        run *= shape[i]
+    s = st[1] if T > 1 else st[0] if B > 1 else inner
+    _need(dense and s >= inner and (B <= 1 or T <= 1 or st[0] == T * s),
+          f"{name}: heads must be dense and tokens evenly spaced (got shape {tuple(shape)}, "
+          f"strides {tuple(st)}); pass {name}.contiguous()")
+    return s
+
+
+def _cuda_device(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    return t.device
+
+
+class _on:
+    """Makes ``device`` current, and ``stream`` where one is given, so that
+    what is allocated meanwhile belongs to the stream that uses it.  Costs
+    nothing where both are current already."""
+
+    def __init__(self, device, stream):
+        self.ctx = []
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            self.ctx.append(torch.cuda.stream(stream))     # sets the device too
+        elif torch.cuda.current_device() != device.index:
+            self.ctx.append(torch.cuda.device(device))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        for c in self.ctx:
+            c.__exit__(*exc)
+
+
+def _rotation(inv_freq, Dk, interleaved, device):
+    _tensor("inv_freq", inv_freq, torch.float32, device)
+    _need(inv_freq.dim() == 1 and inv_freq.is_contiguous(), "inv_freq must be a dense vector")
+    rot = 2 * inv_freq.numel()
+    _need(rot % 16 == 0 and 16 <= rot <= Dk,
+          f"inv_freq must hold rot_dim/2 frequencies, rot_dim a multiple of 16 in [16, {Dk}]")
+    return Rotation(inv_freq.data_ptr(), rot, int(bool(interleaved)))
+
+
+def _token_problem(q_heads, k_heads, B, T, Dk, Dv, cu_seqlens, device, scalar=False):
+    p = Problem(batch=B, seqlen=T, num_q_heads=q_heads, num_kv_heads=k_heads, head_dim_k=Dk,
+                head_dim_v=Dv, flags=FIX_FLAG_SCALAR_GATE if scalar else 0)
+    if cu_seqlens is not None:
+        _tensor("cu_seqlens", cu_seqlens, torch.int64, device)
+        _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2 and cu_seqlens.is_contiguous(),
+              "cu_seqlens must be a dense int64 vector of S + 1 entries")
+        _need(B == 1, "packed sequences use a batch of 1")
+        p.num_seqs = cu_seqlens.numel() - 1
+        p.cu_seqlens = cu_seqlens.data_ptr()
+    return p
+
+
+def fix_attn_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved=False,
+                    inverse=False, out=None, stream=None):
+    """Rotates q [B,T,Hq,Dk] and k [B,T,Hkv,Dk] (or None) by position: the
+    channel pair i at position p turns by p * inv_freq[i] (``inv_freq`` float32
+    [rot_dim/2] on the device; pairs (i, i + rot_dim/2), or (2i, 2i + 1) with
+    ``interleaved``; channels from rot_dim on are copied).  Positions are t,
+    the index within the sequence for packed tokens (B = 1, int64
+    ``cu_seqlens`` on the device; tokens behind the last sequence are copied),
+    or int32 ``positions`` [B,T].  q and k may be views of one projection's
+    output.  ``inverse`` turns back (the gradient).  Returns new dense (q, k),
+    or ``out`` = (q_out, k_out), which may be dense inputs themselves."""
+    dev = _cuda_device("q", q)
+    _tensor("q", q, torch.bfloat16, dev)
+    _need(q.dim() == 4, "q must be [B,T,Hq,Dk]")
+    B, T, Hq, Dk = q.shape
+    Hkv = Hq
+    if k is not None:
+        _tensor("k", k, torch.bfloat16, dev)
+        _need(k.dim() == 4 and k.shape[:2] == q.shape[:2] and k.shape[3] == Dk,
+              "k must be [B,T,Hkv,Dk] with q's B, T and Dk")
+        Hkv = k.shape[2]
+    r = _rotation(inv_freq, Dk, interleaved, dev)
+    p = _token_problem(Hq, Hkv, B, T, Dk, Dk, cu_seqlens, dev)
+    if positions is not None:
+        _dense("positions", positions, torch.int32, dev, q.shape[:2])
+    qs = _token_stride("q", q, Hq * Dk)
+    ks = _token_stride("k", k, Hkv * Dk) if k is not None else 0
+    with _on(dev, stream) as st:
+        if out is None:
+            q_out = torch.empty((B, T, Hq, Dk), dtype=torch.bfloat16, device=dev)
+            k_out = (torch.empty((B, T, Hkv, Dk), dtype=torch.bfloat16, device=dev)
+                     if k is not None else None)
+        else:
+            q_out, k_out = out
+            _dense("out[0]", q_out, torch.bfloat16, dev, q.shape)
+            _need((k is None) == (k_out is None), "out[1] goes with k")
+            if k is not None:
+                _dense("out[1]", k_out, torch.bfloat16, dev, k.shape)
+        s = load().fix_attn_rotary(ctypes.byref(p), ctypes.byref(r), _ptr(positions), _ptr(q), qs,
+                                   _ptr(k), ks, _ptr(q_out), _ptr(k_out), int(bool(inverse)), st)
+    if s != 0:
+        raise FixStatusError(s, "fix_attn_rotary")
+    return q_out, k_out
+
+
+def _page_cache(k_pages, v_pages, g_pages, page_table, seqlens, status, S, dev):
+    _tensor("k_pages", k_pages, torch.bfloat16, dev)
+    _need(k_pages.dim() == 4 and k_pages.is_contiguous(),
+          "k_pages must be a dense [num_pages,page_size,Hkv,Dk]")
+    P, ps, Hkv, _ = k_pages.shape
+    _tensor("v_pages", v_pages, torch.bfloat16, dev)
+    _need(v_pages.dim() == 4 and v_pages.is_contiguous() and v_pages.shape[:3] == k_pages.shape[:3],
+          "v_pages must be a dense [num_pages,page_size,Hkv,Dv]")
+    _tensor("g_pages", g_pages, torch.float32, dev)
+    _need(g_pages.is_contiguous() and (g_pages.shape == v_pages.shape
+                                       or g_pages.shape == v_pages.shape[:3]),
+          "g_pages must be a dense [num_pages,page_size,Hkv,Dv] or [num_pages,page_size,Hkv]")
+    _tensor("page_table", page_table, torch.int32, dev)
+    _need(page_table.dim() == 2 and page_table.is_contiguous() and page_table.shape[0] == S,
+          f"page_table must be a dense [{S},max_pages]")
+    _dense("seqlens", seqlens, torch.int32, dev, (S,))
+    if status is not None:
+        _tensor("status", status, torch.int32, dev)
+        _need(status.numel() == 1, "status must hold one int32")
+    return PageCache(ps, P, page_table.shape[1], page_table.data_ptr(), seqlens.data_ptr(),
+                     k_pages.data_ptr(), v_pages.data_ptr(), g_pages.data_ptr(),
+                     status.data_ptr() if status is not None else None)
+
+
+def fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlens,
+                          cu_seqlens=None, q=None, inv_freq=None, interleaved=False,
+                          return_k=False, status=None, stream=None):
+    """Appends new tokens k [B,T,Hkv,Dk], v [B,T,Hkv,Dv] bf16 and g [B,T,Hkv,Dv]
+    (or [B,T,Hkv]) f32 to a paged cache: k_pages [num_pages,page_size,Hkv,Dk],
+    v_pages and g_pages likewise, int32 ``page_table`` [S,max_pages], int32
+    ``seqlens`` [S] (lengths with the new tokens; S = B, or packed B = 1 with
+    int64 ``cu_seqlens`` [S+1], all on the device).  The last token of
+    sequence b takes position seqlens[b] - 1.  With ``inv_freq`` the keys, and
+    ``q`` [B,T,Hq,Dk], are rotated by position as in ``fix_attn_rotary``.
+    Tokens at negative positions are padding and not stored.  Returns (q, k)
+    rotated: None without ``q`` / unless ``return_k``.  ``status`` (int32 [1])
+    is set to FIX_ERR_PAGE if a token had no page (it is skipped)."""
+    dev = _cuda_device("k", k)
+    _tensor("k", k, torch.bfloat16, dev)
+    _tensor("v", v, torch.bfloat16, dev)
+    _tensor("g", g, torch.float32, dev)
+    _need(k.dim() == 4 and v.dim() == 4 and v.shape[:3] == k.shape[:3],
+          "k and v must be [B,T,Hkv,Dk] and [B,T,Hkv,Dv]")
+    B, T, Hkv, Dk = k.shape
+    Dv = v.shape[3]
+    scalar = g.dim() == 3
+    _need(g.shape == (v.shape[:3] if scalar else v.shape),
+          "g must be [B,T,Hkv,Dv] or [B,T,Hkv]")
+    Hq = Hkv
+    if q is not None:
+        _tensor("q", q, torch.bfloat16, dev)
+        _need(q.dim() == 4 and q.shape[:2] == k.shape[:2] and q.shape[3] == Dk,
+              "q must be [B,T,Hq,Dk] with k's B, T and Dk")
+        Hq = q.shape[2]
+    _need(inv_freq is not None or (q is None and not return_k),
+          "q and return_k go with inv_freq")
+    p = _token_problem(Hq, Hkv, B, T, Dk, Dv, cu_seqlens, dev, scalar)
+    c = _page_cache(k_pages, v_pages, g_pages, page_table, seqlens, status,
+                    p.num_seqs if cu_seqlens is not None else B, dev)
+    _need(k_pages.shape[2:] == k.shape[2:] and v_pages.shape[3] == Dv
+          and (g_pages.dim() == 3) == scalar, "the pages must have the tokens' heads, dims and gate")
+    r = _rotation(inv_freq, Dk, interleaved, dev) if inv_freq is not None else None
+    qs = _token_stride("q", q, Hq * Dk) if q is not None else 0
+    ks = _token_stride("k", k, Hkv * Dk)
+    vs = _token_stride("v", v, Hkv * Dv)
+    gs = _token_stride("g", g, Hkv if scalar else Hkv * Dv)
+    with _on(dev, stream) as st:
+        q_out = (torch.empty((B, T, Hq, Dk), dtype=torch.bfloat16, device=dev)
+                 if q is not None else None)
+        k_out = (torch.empty((B, T, Hkv, Dk), dtype=torch.bfloat16, device=dev)
+                 if return_k else None)
+        s = load().fix_attn_append_paged(
+            ctypes.byref(p), ctypes.byref(c), ctypes.byref(r) if r is not None else None, _ptr(q),
+            qs, _ptr(k), ks, _ptr(v), vs, _ptr(g), gs, _ptr(q_out), _ptr(k_out), st)
+    if s != 0:
+        raise FixStatusError(s, "fix_attn_append_paged")
+    return q_out, k_out
+
+
+def _paged_problem(q, k_pages, v_pages, g_pages, page_table, seqlens, scale, eps, y_dtype, o_norm,
+                   status):
+    dev = _cuda_device("q", q)
+    _tensor("q", q, torch.bfloat16, dev)
+    _need(q.dim() == 3 and q.is_contiguous(), "q must be a dense [B,Hq,Dk]")
+    _need(y_dtype in (torch.bfloat16, torch.float32), "y_dtype must be bfloat16 or float32")
+    B, Hq, Dk = q.shape
+    c = _page_cache(k_pages, v_pages, g_pages, page_table, seqlens, status, B, dev)
+    _need(k_pages.shape[3] == Dk, "q must have the pages' Dk")
+    p = Problem(batch=B, seqlen=1, num_q_heads=Hq, num_kv_heads=k_pages.shape[2], head_dim_k=Dk,
+                head_dim_v=v_pages.shape[3], y_dtype=1 if y_dtype == torch.float32 else 0,
+                flags=(0 if o_norm else FIX_FLAG_NO_NORM)
+                | (FIX_FLAG_SCALAR_GATE if g_pages.dim() == 3 else 0),
+                scale=float(scale) if scale is not None else 0.0, eps=float(eps))
+    return dev, p, c
+
+
+def fix_attn_decode_paged_workspace(q, k_pages, v_pages, g_pages, page_table, seqlens):
+    """A workspace for ``fix_attn_decode_paged`` calls of this shape that do
+    not overlap (uint8 tensor; needs no initialisation)."""
+    dev, p, c = _paged_problem(q, k_pages, v_pages, g_pages, page_table, seqlens, None, 1e-6,
+                               torch.bfloat16, True, None)
+    n = int(load().fix_attn_decode_paged_workspace_bytes(ctypes.byref(p), ctypes.byref(c)))
+    return torch.empty(max(n, 1), device=dev, dtype=torch.uint8)
+
+
+def fix_attn_decode_paged(q, k_pages, v_pages, g_pages, page_table, seqlens, o_norm_weight=None,
+                          scale=None, eps=1e-6, y_dtype=torch.bfloat16, o_gate=None, o_norm=True,
+                          workspace=None, out=None, status=None, stream=None):
+    """One new query per sequence, q [B,Hq,Dk], against a paged cache (see
+    ``fix_attn_append_paged``; the new token is in it): the last row of
+    ``fix_attn`` on each sequence, as ``fix_attn_decode`` computes it from a
+    contiguous cache.  int32 ``seqlens`` [B] on the device; length 0 gives 0.
+    ``status`` (int32 [1]) is set to FIX_ERR_PAGE if a token had no page (it
+    is left out).  Returns y [B,Hq,Dv]."""
+    dev, p, c = _paged_problem(q, k_pages, v_pages, g_pages, page_table, seqlens, scale, eps,
+                               y_dtype, o_norm, status)
+    B, Hq, Dv = p.batch, p.num_q_heads, p.head_dim_v
+    if o_norm:
+        _need(o_norm_weight is not None, "o_norm=True needs o_norm_weight")
+    if o_norm_weight is not None:
+        _dense("o_norm_weight", o_norm_weight, torch.bfloat16, dev, (Dv,))
+    if o_gate is not None:
+        _dense("o_gate", o_gate, torch.bfloat16, dev, (B, Hq, Dv))
+    lib = load()
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((B, Hq, Dv), device=dev, dtype=y_dtype)
+        else:
+            _dense("out", out, y_dtype, dev, (B, Hq, Dv))
+        if workspace is None:
+            nbytes = int(lib.fix_attn_decode_paged_workspace_bytes(ctypes.byref(p),
+                                                                   ctypes.byref(c)))
+            workspace = torch.empty(max(nbytes, 1), device=dev, dtype=torch.uint8)
+        else:
+            _tensor("workspace", workspace, torch.uint8, dev)
+            _need(workspace.is_contiguous(), "workspace must be contiguous")
+        s = lib.fix_attn_decode_paged(ctypes.byref(p), ctypes.byref(c), _ptr(q),
+                                      _ptr(o_norm_weight), _ptr(o_gate), _ptr(out),
+                                      _ptr(workspace), workspace.numel(), st)
+    if s != 0:
+        raise FixStatusError(s, "fix_attn_decode_paged")
+    return out
+
+
 def fix_attn_device_status(workspace, stream=None) -> int:
     return int(load().fix_attn_device_status(_ptr(workspace), _stream(stream)))
 
@@ -325,6 +635,30 @@ class _FixAttn(torch.autograd.Function):
             _check(ctx.ws, "fix_attn backward (device status)")
         ctx.ws = None
         return dq, dk, dv, dg, dw, dz, None, None, None, None, None, None, None
+
+
+class _FixRotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, inv_freq, cu_seqlens, positions, interleaved, inverse):
+        ctx.save_for_backward(inv_freq, cu_seqlens, positions)
+        ctx.cfg = (interleaved, not inverse)
+        return fix_attn_rotary(q, k, inv_freq, cu_seqlens, positions, interleaved, inverse)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        # the rotation is linear and orthogonal: its gradient is the rotation
+        # back, itself differentiable
+        dq, dk = _FixRotary.apply(dq.contiguous(), dk.contiguous(), *ctx.saved_tensors,
+                                  *ctx.cfg)
+        return dq, dk, None, None, None, None, None
+
+
+def fix_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved=False):
+    """``fix_attn_rotary`` of q and k, differentiable in both: the rotation
+    that a model trains with before ``fix_attn``, the same that
+    ``fix_attn_append_paged`` applies when it serves."""
+    _need(k is not None, "fix_rotary needs q and k")
+    return _FixRotary.apply(q, k, inv_freq, cu_seqlens, positions, bool(interleaved), False)
 
 
 def fix_attn(q, k, v, g, o_norm_weight=None, cu_seqlens=None, cu_seqlens_host=None, scale=None,

@@ -59,7 +59,8 @@ typedef enum {
   FIX_ERR_DTYPE = 8,           /* unknown y_dtype / algo */
   FIX_ERR_CUDA = 9,            /* a CUDA runtime call or launch failed */
   FIX_ERR_DEVICE_TIMEOUT = 10, /* a bounded device wait expired (see above) */
-  FIX_ERR_ARCH = 11            /* the current device is not sm_100 */
+  FIX_ERR_ARCH = 11,           /* the current device is not sm_100 */
+  FIX_ERR_PAGE = 12            /* device side only: see fix_attn_page_cache.status */
 } fix_status;
 
 enum { FIX_DTYPE_BF16 = 0, FIX_DTYPE_F32 = 1 };
@@ -197,6 +198,107 @@ fix_status fix_attn_decode(const fix_attn_problem *p, const int32_t *seqlens, co
                            const void *k_cache, const void *v_cache, const float *g_cache,
                            const void *o_norm_weight, const void *o_gate, void *y,
                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Rotation of q and k by position (rotary embedding).  The pair (a, b) of
+ * pair index i at position p turns by the angle t = p * inv_freq[i]:
+ *     a' = a cos t - b sin t,   b' = a sin t + b cos t
+ * (the angle is formed in double precision, so far positions keep theirs).
+ * The pairs are channels (i, i + rot_dim/2), or (2i, 2i + 1) with
+ * `interleaved`; channels from rot_dim on are copied.  (The FiX poster
+ * abstract calls the gate complementary to a rotation of queries and keys,
+ * which the caller applies before the attention.) */
+typedef struct {
+  const float *inv_freq;  /* device f32 [rot_dim/2], 16-byte aligned          */
+  int32_t rot_dim;        /* rotated channels: a multiple of 16 in [16, Dk]   */
+  int32_t interleaved;    /* 0: pairs (i, i + rot_dim/2); 1: (2i, 2i + 1)      */
+} fix_attn_rotation;
+
+/* Rotates q (and k) of N tokens.
+ *   q [N,Hq,Dk], k [N,Hkv,Dk] bf16 -> q_out [N,Hq,Dk], k_out [N,Hkv,Dk] bf16
+ * The inputs' heads are dense, and consecutive tokens lie q_stride / k_stride
+ * elements apart (0: dense; else a multiple of 8, at least H*Dk), so q and k
+ * may be views of one projection's output.  The outputs are dense and may be
+ * the (dense) inputs themselves.  k and k_out may both be NULL.
+ * Positions: `positions` (device int32 [N]) where given; else the index
+ * within the sequence, i.e. t in [B,T] or n - cu_seqlens[b] when packed.
+ * Packed: problem.cu_seqlens (device) is read, cu_seqlens_host may be NULL
+ * (nothing is planned on the host); tokens behind the last sequence are
+ * copied without a rotation.
+ * `inverse` != 0 turns by -t: the gradient, and the inverse. */
+fix_status fix_attn_rotary(const fix_attn_problem *p, const fix_attn_rotation *r,
+                           const int32_t *positions, const void *q, int64_t q_stride,
+                           const void *k, int64_t k_stride, void *q_out, void *k_out,
+                           int inverse, void *stream);
+
+/* A paged cache of keys, values and log forget gates.  Token `pos` of
+ * sequence b lives in slot pos % page_size of page page_table[b][pos /
+ * page_size]; the pages hold
+ *   k_pages [num_pages,page_size,Hkv,Dk] bf16,
+ *   v_pages [num_pages,page_size,Hkv,Dv] bf16,
+ *   g_pages [num_pages,page_size,Hkv,Dv] f32 ([num_pages,page_size,Hkv] with
+ *           FIX_FLAG_SCALAR_GATE).
+ * num_pages * page_size * Hkv must stay below 2^32.  Table entries that no
+ * token needs are not used (any value may stand there). */
+typedef struct {
+  int32_t page_size;          /* tokens per page, >= 1                         */
+  int32_t num_pages;          /* pages in the pools                            */
+  int32_t max_pages;          /* columns of the page table                     */
+  const int32_t *page_table;  /* device [S,max_pages]                          */
+  const int32_t *seqlens;     /* device [S]: tokens per sequence, those of this
+                                 call included                                 */
+  void *k_pages;
+  void *v_pages;
+  float *g_pages;
+  int32_t *status;            /* device int32 or NULL: set to FIX_ERR_PAGE when
+                                 a token that was needed has no page (a length
+                                 beyond the table's columns, or a page id
+                                 outside [0, num_pages)); never reset here.
+                                 Such a token is skipped: nothing is read or
+                                 written outside the pools.                    */
+} fix_attn_page_cache;
+
+/* Appends new tokens to the cache, rotating their keys (and queries) on the
+ * way.  problem: batch = B sequences of seqlen = T new tokens each (S = B), or
+ * packed with batch = 1, seqlen = N and cu_seqlens (device [S+1], num_seqs =
+ * S; cu_seqlens_host may be NULL: lengths are read on the device only, so a
+ * captured call may be replayed with others).
+ *   k [N,Hkv,Dk], v [N,Hkv,Dv] bf16, g [N,Hkv,Dv] f32 ([N,Hkv] with the
+ *   scalar gate): the new tokens, strides as in fix_attn_rotary (v_stride a
+ *   multiple of 8, g_stride of 4; any g_stride >= Hkv with the scalar gate).
+ * The n_b new tokens of sequence b take positions seqlens[b] - n_b ..
+ * seqlens[b] - 1, and the angles of `r` go by these.  A token whose position
+ * is negative is padding (a row of a fixed-size batch whose seqlens is 0): it
+ * is not stored.  Tokens behind the last sequence are not stored either; all
+ * other slots of the pages stay as they were.
+ *   r: NULL stores k as it is (q, q_out and k_out must then be NULL).
+ *   q [N,Hq,Dk] / q_out [N,Hq,Dk]: NULL, or queries to rotate likewise.
+ *   k_out [N,Hkv,Dk]: NULL, or receives the rotated keys densely (for the
+ *   prompt's fix_attn_fwd).  Rows of tokens without a position are copied to
+ *   q_out and k_out without a rotation.
+ * Two tokens of one call must not share a slot (which one it then holds is
+ * unspecified). */
+fix_status fix_attn_append_paged(const fix_attn_problem *p, const fix_attn_page_cache *c,
+                                 const fix_attn_rotation *r, const void *q, int64_t q_stride,
+                                 const void *k, int64_t k_stride, const void *v,
+                                 int64_t v_stride, const float *g, int64_t g_stride,
+                                 void *q_out, void *k_out, void *stream);
+
+/* fix_attn_decode over a paged cache: one new query per sequence against
+ * tokens 0 .. seqlens[b] - 1 of its pages (the new token, appended before,
+ * included; keys rotated where q is).  problem: batch = B, seqlen = 1, heads,
+ * head dims, scale, eps, y_dtype, FIX_FLAG_NO_NORM / FIX_FLAG_SCALAR_GATE.
+ *   q [B,Hq,Dk] bf16, o_norm_weight, o_gate, y as in fix_attn_decode.
+ * A sequence of length 0 gives y = 0.  Slots past a sequence's length are
+ * never read.  Any Hq/Hkv.  The work is split over the cache on the device by
+ * the lengths found there, so a captured call may be replayed with others.
+ * The workspace needs no initialisation; calls that may overlap need one
+ * each. */
+size_t fix_attn_decode_paged_workspace_bytes(const fix_attn_problem *p,
+                                             const fix_attn_page_cache *c);
+fix_status fix_attn_decode_paged(const fix_attn_problem *p, const fix_attn_page_cache *c,
+                                 const void *q, const void *o_norm_weight, const void *o_gate,
+                                 void *y, void *workspace, size_t workspace_bytes,
+                                 void *stream);
 
 /* Synchronises `stream`, then returns the device status word that the last
  * call on this workspace left (FIX_OK or FIX_ERR_DEVICE_TIMEOUT), or
