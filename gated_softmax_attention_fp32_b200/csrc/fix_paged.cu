@@ -12,26 +12,25 @@
 //
 // Work split (paged_decode_kernel).  A unit is one (sequence, kv head, block
 // of up to 8 NT q heads of its group); its keys are cut into tiles of 16.
-// All units' tiles form one line, cut into equal spans, one per warp of the
-// grid: unequal lengths balance, and the lengths are read on the device.  A
-// warp works alone (own ring of tiles in shared memory, no block barriers),
-// newest tile first, so that the decay is a running suffix sum of the gates
-// and no factor exceeds 1 for g <= 0.  A piece that is a whole unit is
-// finished by its warp; the others leave (m, l, o, total gate) in a slot of
-// the workspace and paged_join_kernel joins a unit's pieces: the decay from a
-// piece's last key to t is exp(the later pieces' gate totals).
+// All units form one line, a unit taking a position per tile and kUnitCost
+// more for what a warp spends on starting and finishing it; the line is cut
+// into equal spans, one per warp of the grid, so that unequal lengths balance
+// (they are read on the device).  A warp works alone (own ring of tiles in
+// shared memory, no block barriers), newest tile first, so that the decay is
+// a running suffix sum of the gates and no factor exceeds 1 for g <= 0.  A
+// unit that lies in one span is finished by its warp; the pieces of the
+// others leave (m, l, o, total gate) in the workspace, and paged_join_kernel
+// joins them: the decay from a piece's last key to t is exp(the later pieces'
+// gate totals).
 //
 // Matrix products (mma.sync: a tile has 16 keys and 8 heads, far too few rows
-// for tcgen05 to pay).  Keys take the 16-row side in S^T = K q^T and the
-// reduced side in O^T = V'^T P^T, heads the 8 columns.  The reduced side may
-// be permuted freely: lane j of four takes keys 4j..4j+3, so that a suffix sum
-// over the tile's gates is three additions in a lane and a scan over four
-// lanes.  Row r of the S product is therefore key 4 (r / 2) + r % 2, and + 2
-// for r >= 8.
+// for tcgen05 to pay).  Keys take the 16-row side in S^T = K q^T, value
+// channels in O^T = V'^T P^T, heads the 8 columns.
 // Precision: q k products are exact in the bf16 product and summed in fp32.
 // Element-wise gate: V' = D v and P are fp32 values, split into two tf32
 // parts each (11 bits and more), three products: about 2^-21.  Scalar gate:
 // V stays bf16, D goes to P, which is split into three bf16 parts (24 bits).
+// Gate sums are kept in units of log 2.
 #include "fix_internal.h"
 
 #define FIX_PAGED_TRY(expr)           \
@@ -46,6 +45,7 @@ constexpr int kTileKeys = 16;
 constexpr int kPagedWarps = 4;         // warps per CTA of the split kernel
 constexpr int kJoinThreads = 256;
 constexpr int kSMs = 148;              // B200
+constexpr int kUnitCost = 2;           // line positions of a unit beside its tiles
 
 struct PagedArgs {
   int B, Hq, Hkv, Dk, grp, no_norm, y_f32;
@@ -60,6 +60,7 @@ struct PagedArgs {
   int nworkers;
   long long slot_floats;               // floats per slot: hpb (DV + 2) + DV
   float* slots;                        // two per worker
+  int4* jobs;                          // the join's work: (pieces, first worker, unit)
   int units;                           // B * Hkv * nhb
   int join_by_unit, heads_per_cta;     // shape of the join
 };
@@ -72,55 +73,50 @@ __device__ __forceinline__ int paged_len(const PagedArgs& a, int b) {
 __device__ __forceinline__ int paged_tiles(const PagedArgs& a, int b) {
   return (int)(((unsigned)paged_len(a, b) + kTileKeys - 1) / kTileKeys);
 }
-__device__ __forceinline__ long long warp_sum_ll(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// Line positions of one unit of sequence b.
+__device__ __forceinline__ int paged_cost(const PagedArgs& a, int b) {
+  const int n = paged_tiles(a, b);
+  return n ? n + kUnitCost : 0;
 }
 
-// Tiles of one head block over all sequences (whole warp).
-__device__ __forceinline__ long long tiles_total(const PagedArgs& a) {
-  long long n = 0;
+// The line over all sequences, for a whole warp: lane i sums a run of K
+// sequences, their positions per unit.
+struct Line {
+  int K;
+  long long mine, upto;        // of this lane's run; of the runs up to it
+  __device__ __forceinline__ explicit Line(const PagedArgs& a) {
+    const int lane = threadIdx.x & 31;
+    K = (a.B + 31) / 32;
+    mine = 0;
 #pragma unroll 8
-  for (int b = threadIdx.x & 31; b < a.B; b += 32) n += paged_tiles(a, b);
-  return warp_sum_ll(n);
-}
-// Tiles of one head block before sequence b (whole warp).
-__device__ __forceinline__ long long tiles_before(const PagedArgs& a, int b) {
-  long long n = 0;
-#pragma unroll 8
-  for (int i = threadIdx.x & 31; i < b; i += 32) n += paged_tiles(a, i);
-  return warp_sum_ll(n);
-}
-// The sequence that holds tile `pos` of the line (pos below its length, a
-// line of `upb` units per sequence) and the line position where it starts
-// (whole warp).
-__device__ __forceinline__ void find_tile(const PagedArgs& a, long long pos, int upb, int* b,
-                                          long long* start) {
-  const int lane = threadIdx.x & 31;
-  const int K = (a.B + 31) / 32;                  // sequences per lane
-  long long n = 0;
-#pragma unroll 8
-  for (int i = lane * K; i < min(a.B, (lane + 1) * K); ++i) n += paged_tiles(a, i);
-  n *= upb;
-  long long incl = n;
+    for (int i = lane * K; i < min(a.B, (lane + 1) * K); ++i) mine += paged_cost(a, i);
+    upto = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
   }
-  const int src = __ffs(__ballot_sync(0xffffffffu, incl > pos)) - 1;
-  long long at = __shfl_sync(0xffffffffu, incl - n, src);
-  int i = src * K;
-  for (;;) {
-    const long long t = (long long)paged_tiles(a, i) * upb;
-    if (pos < at + t || i + 1 >= a.B) break;
-    at += t;
-    ++i;
+  __device__ __forceinline__ long long total() const {
+    return __shfl_sync(0xffffffffu, upto, 31);
   }
-  *b = i;
-  *start = at;
-}
+  // The sequence that holds position pos < total() * upb of the line of upb
+  // units per sequence, and where it starts.
+  __device__ __forceinline__ void find(const PagedArgs& a, long long pos, int upb, int* b,
+                                       long long* start) const {
+    const int src = __ffs(__ballot_sync(0xffffffffu, upto * upb > pos)) - 1;
+    long long at = __shfl_sync(0xffffffffu, (upto - mine) * upb, src);
+    int i = src * K;
+    for (;;) {
+      const long long t = (long long)paged_cost(a, i) * upb;
+      if (pos < at + t || i + 1 >= a.B) break;
+      at += t;
+      ++i;
+    }
+    *b = i;
+    *start = at;
+  }
+};
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -201,11 +197,56 @@ struct Ring {
   }
 };
 
-// Finishes one row's channel value.
-__device__ __forceinline__ void store_y(const PagedArgs& a, size_t at, float y) {
-  if (a.z) y *= swish(bf2f(a.z[at]));
-  if (a.y_f32) reinterpret_cast<float*>(a.y)[at] = y;
-  else reinterpret_cast<__nv_bfloat16*>(a.y)[at] = f2bf(y);
+// The N channels of one lane of a finished row: y = o f [w] [swish(z)].
+template <int N>
+__device__ __forceinline__ void store_row(const PagedArgs& a, size_t row0, int c0, const float* o,
+                                          float f, bool none) {
+  float y[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    y[e] = o[e] * f;
+    if (!a.no_norm) y[e] *= bf2f(a.w[c0 + e]);
+    if (none) y[e] = 0.f;
+    if (a.z) y[e] *= swish(bf2f(a.z[row0 + c0 + e]));
+  }
+  if (a.y_f32) {
+    float* d = reinterpret_cast<float*>(a.y) + row0 + c0;
+    if constexpr (N == 4) *reinterpret_cast<float4*>(d) = make_float4(y[0], y[1], y[2], y[3]);
+    else if constexpr (N == 2) *reinterpret_cast<float2*>(d) = make_float2(y[0], y[1]);
+    else *d = y[0];
+  } else {
+    __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(a.y) + row0 + c0;
+    if constexpr (N == 4) *reinterpret_cast<uint2*>(d) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+    else if constexpr (N == 2) *reinterpret_cast<uint32_t*>(d) = pack2(y[0], y[1]);
+    else *d = f2bf(y[0]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_n(const float* p, float* x) {
+  if constexpr (N == 4) {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+  } else if constexpr (N == 2) {
+    const float2 u = *reinterpret_cast<const float2*>(p);
+    x[0] = u.x; x[1] = u.y;
+  } else {
+    x[0] = *p;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_n(float* p, const float* x) {
+  if constexpr (N == 4) *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  else if constexpr (N == 2) *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+  else *p = x[0];
+}
+// The factor that finishes a row: 1 / rms of its channels, or 1 / l.
+template <int N>
+__device__ __forceinline__ float row_factor(const PagedArgs& a, const float* o, float l, int DV) {
+  if (a.no_norm) return 1.f / l;
+  float sq = 0.f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) sq += o[e] * o[e];
+  return 1.f / sqrtf(warp_sum(sq) / (float)DV + a.eps);
 }
 
 template <int DV, int NT, bool SCALAR>
@@ -214,6 +255,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
   using R = Ring<DV, SCALAR>;
   constexpr int ST = R::kStages;
   constexpr int MT = DV / 16;
+  constexpr int VPL = DV >= 32 ? DV / 32 : 1;      // channels per lane where lanes span a row
   extern __shared__ __align__(128) char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int Dk = a.Dk;
@@ -222,11 +264,13 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
   const uint32_t ring = smem_addr(mine);
   const int stage_bytes = R::stage(Dk);
   char* sq = mine + ST * stage_bytes;
+  const int upb = a.Hkv * a.nhb;
 
   // sequences without a token
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    if (a.seqlens[b] > 0) {
-      if (a.status && threadIdx.x == 0 && a.seqlens[b] > (long long)a.max_pages * a.page_size)
+    const int L = a.seqlens[b];
+    if (L > 0) {
+      if (a.status && threadIdx.x == 0 && L > (long long)a.max_pages * a.page_size)
         *a.status = FIX_ERR_PAGE;
       continue;
     }
@@ -235,39 +279,49 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
       if (a.y_f32) reinterpret_cast<float*>(a.y)[at] = 0.f;
       else reinterpret_cast<__nv_bfloat16*>(a.y)[at] = f2bf(0.f);
     }
+    if (a.join_by_unit)
+      for (int u = threadIdx.x; u < upb; u += blockDim.x)
+        a.jobs[b * upb + u] = make_int4(0, 0, 0, 0);
   }
 
-  const int upb = a.Hkv * a.nhb;
-  const long long total = tiles_total(a) * upb;
+  const Line line(a);
+  const long long total = line.total() * upb;
   const int worker = warp * gridDim.x + blockIdx.x;
   const long long span = (total + a.nworkers - 1) / a.nworkers;
   const long long first = span * worker, last = min(total, first + span);
-  if (first >= last) return;
-  int b;
-  long long base;                     // line position of sequence b
-  find_tile(a, first, upb, &b, &base);
+  int4 job = make_int4(0, 0, 0, 0);      // the unit that begins here and ends beyond
+  int b = 0;
+  long long base = 0;                    // line position of sequence b
+  if (first < last) line.find(a, first, upb, &b, &base);
 
   // lane roles
   const int j = lane & 3, r8 = lane & 7;
-  const int ldkey = ((r8 >> 1) << 2) | (r8 & 1);            // key of matrix row r8
-  const uint32_t kaddr = (uint32_t)(ldkey + ((lane >> 3) & 1) * 2) * kpitch;
+  const uint32_t kaddr = (uint32_t)(r8 + ((lane >> 3) & 1) * 8) * kpitch;
   const int kchunk = lane >> 4;
-  const uint32_t vaddr = (uint32_t)(ldkey + (lane >> 4) * 2) * R::kVPitch;
+  const uint32_t vaddr = (uint32_t)(r8 + (lane >> 4) * 8) * R::kVPitch;
   const int vchunk = (lane >> 3) & 1;
-  const int key0 = ((lane >> 3) << 2) | ((lane >> 2) & 1);  // keys of this lane's two S rows
+  const int key0 = lane >> 2;                               // and key0 + 8: the S rows
   const int kshift = 31 - __clz(Dk / 8);
+  const bool whole_pages = a.page_size % kTileKeys == 0;    // a tile lies in one page
 
   for (long long pos = first; pos < last;) {
     const int L = paged_len(a, b);
     const int nb = (int)(((unsigned)L + kTileKeys - 1) / kTileKeys);
-    if (pos >= base + (long long)nb * upb) {                // next sequence
-      base += (long long)nb * upb;
+    const int cost = nb ? nb + kUnitCost : 0;
+    if (pos >= base + (long long)cost * upb) {              // next sequence
+      base += (long long)cost * upb;
       ++b;
       continue;
     }
-    const int u = (int)((pos - base) / nb);                 // unit of the sequence
-    const int t0 = (int)((pos - base) - (long long)u * nb);
-    const int t1 = (int)min((long long)nb, t0 + (last - pos));
+    const int u = (int)((pos - base) / cost);               // unit of the sequence
+    const long long live = base + (long long)u * cost + kUnitCost;   // position of its tile 0
+    const int t0 = (int)max(0LL, pos - live);
+    const int t1 = (int)min((long long)nb, last - live);
+    pos = live + max(t0, t1);
+    if (t1 <= t0) {
+      if (pos > last) break;
+      continue;
+    }
     const int kv = u / a.nhb, hb = u - kv * a.nhb;
     const int h0 = kv * a.grp + hb * a.hpb;                 // first q head
     const int nh = min(a.hpb, a.grp - hb * a.hpb);          // q heads
@@ -291,51 +345,82 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
       row = page < 0 ? 0u : ((uint32_t)page * a.page_size + slot) * a.Hkv + kv;
       mask = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
     };
+    // Tiles go to shared memory in rows of keys, 16-byte chunk c of key s at
+    // chunk c ^ (s % 8): matrix loads and the gates' reads meet no conflicts.
+    // A full tile of one page has evenly spaced rows; keys that are not there
+    // are filled with zeros.
     auto copy_k = [&](int stage, uint32_t row, uint32_t mask) {
       const uint32_t dst = ring + stage * stage_bytes;
+      const int c = lane & ((1 << kshift) - 1), per = 32 >> kshift;
+      int key = lane >> kshift;
+      if (whole_pages && mask == 0xffffu) {
+        const __nv_bfloat16* src =
+            a.k + (size_t)(__shfl_sync(0xffffffffu, row, 0) + key * a.Hkv) * Dk + c * 8;
+        const size_t step = (size_t)per * a.Hkv * Dk;
 #pragma unroll 8
-      for (int it = 0; it < Dk / 16; ++it) {
-        const int idx = it * 32 + lane, key = idx >> kshift, c = idx & ((1 << kshift) - 1);
-        const uint32_t rr = __shfl_sync(0xffffffffu, row, key);
-        const int f = ((key >> 2) << 1) | (key & 1);
-        copy16(dst + key * kpitch + ((c ^ f) << 4), a.k + (size_t)rr * Dk + c * 8,
-               (mask >> key) & 1);
+        for (int it = 0; it < Dk / 16; ++it, key += per, src += step)
+          copy16(dst + key * kpitch + ((c ^ (key & 7)) << 4), src, true);
+      } else {
+#pragma unroll 1
+        for (int it = 0; it < Dk / 16; ++it, key += per) {
+          const uint32_t rr = __shfl_sync(0xffffffffu, row, key);
+          copy16(dst + key * kpitch + ((c ^ (key & 7)) << 4), a.k + (size_t)rr * Dk + c * 8,
+                 (mask >> key) & 1);
+        }
       }
     };
     auto copy_vg = [&](int stage, uint32_t row, uint32_t mask) {
       const uint32_t dst = ring + stage * stage_bytes + kTileKeys * kpitch;
-#pragma unroll
-      for (int it = 0; it < DV / 16; ++it) {
-        const int idx = it * 32 + lane, key = idx / (DV / 8), c = idx % (DV / 8);
-        const uint32_t rr = __shfl_sync(0xffffffffu, row, key);
-        const int f = ((key >> 2) << 1) | (key & 1);
-        copy16(dst + key * R::kVPitch + ((c ^ f) << 4), a.v + (size_t)rr * DV + c * 8,
-               (mask >> key) & 1);
-      }
       const uint32_t gdst = dst + R::kV;
-      if (SCALAR) {
-        if (lane < kTileKeys) copy4(gdst + lane * 4, a.g + row, (mask >> lane) & 1);
-      } else {
+      constexpr int CV = DV / 8, CG = DV / 4;               // chunks per row
+      const int vc = lane % CV, gc = lane % CG;
+      if (whole_pages && mask == 0xffffu) {
+        const uint32_t row0 = __shfl_sync(0xffffffffu, row, 0);
+        const __nv_bfloat16* src = a.v + (size_t)(row0 + (lane / CV) * a.Hkv) * DV + vc * 8;
+        const size_t vstep = (size_t)(32 / CV) * a.Hkv * DV;
 #pragma unroll
-        for (int it = 0; it < DV / 8; ++it) {
-          const int idx = it * 32 + lane, key = idx / (DV / 4), c = idx % (DV / 4);
+        for (int it = 0; it < DV / 16; ++it, src += vstep) {
+          const int key = it * (32 / CV) + lane / CV;
+          copy16(dst + key * R::kVPitch + ((vc ^ (key & 7)) << 4), src, true);
+        }
+        if constexpr (!SCALAR) {
+          const float* gs = a.g + (size_t)(row0 + (lane / CG) * a.Hkv) * DV + gc * 4;
+          const size_t gstep = (size_t)(32 / CG) * a.Hkv * DV;
+#pragma unroll
+          for (int it = 0; it < DV / 8; ++it, gs += gstep) {
+            const int key = it * (32 / CG) + lane / CG;
+            copy16(gdst + key * R::kGPitch + ((gc ^ (key & 7)) << 4), gs, true);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int it = 0; it < DV / 16; ++it) {
+          const int key = it * (32 / CV) + lane / CV;
           const uint32_t rr = __shfl_sync(0xffffffffu, row, key);
-          copy16(gdst + key * R::kGPitch + ((c ^ ((key >> 2) << 1)) << 4),
-                 a.g + (size_t)rr * DV + c * 4, (mask >> key) & 1);
+          copy16(dst + key * R::kVPitch + ((vc ^ (key & 7)) << 4), a.v + (size_t)rr * DV + vc * 8,
+                 (mask >> key) & 1);
+        }
+        if constexpr (!SCALAR) {
+#pragma unroll 1
+          for (int it = 0; it < DV / 8; ++it) {
+            const int key = it * (32 / CG) + lane / CG;
+            const uint32_t rr = __shfl_sync(0xffffffffu, row, key);
+            copy16(gdst + key * R::kGPitch + ((gc ^ (key & 7)) << 4), a.g + (size_t)rr * DV + gc * 4,
+                   (mask >> key) & 1);
+          }
         }
       }
+      if constexpr (SCALAR)
+        if (lane < kTileKeys) copy4(gdst + lane * 4, a.g + row, (mask >> lane) & 1);
     };
 
     uint32_t row, mask, masks[ST];
     lookup(t1 - 1, row, mask);
     // the block's queries, rows of 8 NT heads (zero beyond nh)
-    __syncwarp();
     for (int i = lane; i < NT * 8 << kshift; i += 32) {
       const int h = i >> kshift, c = i & ((1 << kshift) - 1);
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (h < nh)
-        x = *reinterpret_cast<const uint4*>(a.q + ((size_t)b * a.Hq + h0 + h) * Dk + c * 8);
-      *reinterpret_cast<uint4*>(sq + h * qpitch + c * 16) = x;
+      copy16(smem_addr(sq + h * qpitch + c * 16),
+             a.q + ((size_t)b * a.Hq + h0 + min(h, nh - 1)) * Dk + c * 8, h < nh);
     }
 #pragma unroll
     for (int s = 0; s < ST; ++s) {
@@ -348,8 +433,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
     }
 
     float acc[MT][NT][4];
-    float m[NT][2], l[NT][2];
-    float suf[SCALAR ? 1 : MT][2];
+    float m[NT][2], l[NT][2], suf[VPL];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -364,7 +448,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
         l[t][e] = 0.f;
       }
 #pragma unroll
-    for (int i = 0; i < (SCALAR ? 1 : MT); ++i) suf[i][0] = suf[i][1] = 0.f;
+    for (int e = 0; e < VPL; ++e) suf[e] = 0.f;
 
     for (int i = 0; i < n; ++i) {
       const int stage = ST == 1 ? 0 : (i & 1);
@@ -403,7 +487,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
         for (int e = 0; e < 4; ++e) s[t][e] *= a.scale_log2;
         if (vm != 0xffffu) {
           if (!((vm >> key0) & 1)) s[t][0] = s[t][1] = -INFINITY;
-          if (!((vm >> (key0 + 2)) & 1)) s[t][2] = s[t][3] = -INFINITY;
+          if (!((vm >> (key0 + 8)) & 1)) s[t][2] = s[t][3] = -INFINITY;
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -433,10 +517,10 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
       cp_async_wait<2 * ST - 1>();
       __syncwarp();
       const uint32_t vat = at + kTileKeys * kpitch;
-      const char* gat = mine + stage * stage_bytes + kTileKeys * kpitch + R::kV;
+      char* gat = mine + stage * stage_bytes + kTileKeys * kpitch + R::kV;
       if constexpr (SCALAR) {
         // the decay of key (lane & 15), exp of the gates after it, goes to P
-        float x = reinterpret_cast<const float*>(gat)[lane & 15];
+        float x = reinterpret_cast<const float*>(gat)[lane & 15] * kLog2e;
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) {
           const float z = __shfl_down_sync(0xffffffffu, x, o, 16);
@@ -444,9 +528,9 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
         }
         float after = __shfl_down_sync(0xffffffffu, x, 1, 16);
         if ((lane & 15) == 15) after = 0.f;
-        const float d = ex2((suf[0][0] + after) * kLog2e);
-        suf[0][0] += __shfl_sync(0xffffffffu, x, 0, 16);
-        const float d0 = __shfl_sync(0xffffffffu, d, key0), d1 = __shfl_sync(0xffffffffu, d, key0 + 2);
+        const float d = ex2(suf[0] + after);
+        suf[0] += __shfl_sync(0xffffffffu, x, 0, 16);
+        const float d0 = __shfl_sync(0xffffffffu, d, key0), d1 = __shfl_sync(0xffffffffu, d, key0 + 8);
         uint32_t pb[NT][3][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -474,8 +558,26 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
               mma_bf16(acc[x][t], va, pb[t][part][0], pb[t][part][1]);
         }
       } else {
+        // gates -> decays in place, a lane on its channels from the newest key
+        // back
+        if (DV >= 32 || lane < DV) {
+          char* gl = gat + (VPL == 4 ? 0 : (lane * VPL % 4) * 4);
+          const int gch = lane * VPL / 4;
+#pragma unroll
+          for (int key = kTileKeys - 1; key >= 0; --key) {
+            float* gp = reinterpret_cast<float*>(gl + key * R::kGPitch + ((gch ^ (key & 7)) << 4));
+            float x[VPL], d[VPL];
+            load_n<VPL>(gp, x);
+#pragma unroll
+            for (int e = 0; e < VPL; ++e) {
+              d[e] = ex2(suf[e]);
+              suf[e] = fmaf(x[e], kLog2e, suf[e]);
+            }
+            store_n<VPL>(gp, d);
+          }
+        }
         // P^T: the exact fp32 values, transposed as two 16-bit halves
-        uint32_t ph[NT][4], pl[NT][4];                       // keys 4j .. 4j + 3
+        uint32_t ph[NT][4], pl[NT][4];                       // keys 2j, 2j + 1, 2j + 8, 2j + 9
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -487,6 +589,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
             split_tf32(__uint_as_float(__byte_perm(lo, hi, 0x7632)), ph[t][2 * hf + 1],
                        pl[t][2 * hf + 1]);
           }
+        __syncwarp();
 #pragma unroll
         for (int x = 0; x < MT; ++x) {
           uint32_t va[4];
@@ -494,26 +597,19 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
           uint32_t vh[8], vl[8];            // [2 key + channel half]
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) {
-            const char* gp = gat + 4 * j * R::kGPitch +
-                             (((x * 4 + (lane >> 4) + 2 * ch) ^ (2 * j)) << 4) + ((lane >> 2) & 3) * 4;
-            float gk[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) gk[y] = *reinterpret_cast<const float*>(gp + y * R::kGPitch);
-            const float e2 = gk[3], e1 = e2 + gk[2], e0 = e1 + gk[1];
-            float z, sum = e0 + gk[0];
-            z = __shfl_down_sync(0xffffffffu, sum, 1, 4);
-            if (j < 3) sum += z;
-            z = __shfl_down_sync(0xffffffffu, sum, 2, 4);
-            if (j < 2) sum += z;
-            float after = __shfl_down_sync(0xffffffffu, sum, 1, 4);
-            if (j == 3) after = 0.f;
-            after = (after + suf[x][ch]) * kLog2e;
-            suf[x][ch] += __shfl_sync(0xffffffffu, sum, 0, 4);
+            const char* gp = gat + 2 * j * R::kGPitch + ((lane >> 2) & 3) * 4;
+            const int c = x * 4 + (lane >> 4) + 2 * ch;
             const float2 v01 = unpack2(va[ch]), v23 = unpack2(va[2 + ch]);
-            split_tf32(v01.x * ex2(fmaf(e0, kLog2e, after)), vh[ch], vl[ch]);
-            split_tf32(v01.y * ex2(fmaf(e1, kLog2e, after)), vh[2 + ch], vl[2 + ch]);
-            split_tf32(v23.x * ex2(fmaf(e2, kLog2e, after)), vh[4 + ch], vl[4 + ch]);
-            split_tf32(v23.y * ex2(after), vh[6 + ch], vl[6 + ch]);
+            const float d0 = *reinterpret_cast<const float*>(gp + ((c ^ (2 * j)) << 4));
+            const float d1 =
+                *reinterpret_cast<const float*>(gp + R::kGPitch + ((c ^ (2 * j + 1)) << 4));
+            const float d2 = *reinterpret_cast<const float*>(gp + 8 * R::kGPitch + ((c ^ (2 * j)) << 4));
+            const float d3 =
+                *reinterpret_cast<const float*>(gp + 9 * R::kGPitch + ((c ^ (2 * j + 1)) << 4));
+            split_tf32(v01.x * d0, vh[ch], vl[ch]);
+            split_tf32(v01.y * d1, vh[2 + ch], vl[2 + ch]);
+            split_tf32(v23.x * d2, vh[4 + ch], vl[4 + ch]);
+            split_tf32(v23.y * d3, vh[6 + ch], vl[6 + ch]);
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -533,136 +629,92 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
       if (i + ST + 1 < n) lookup(t1 - 2 - ST - i, row, mask);
     }
 
+    // The piece's rows go through the ring (its tiles are used up), so that
+    // lanes span a row: o [heads][DV + 4], then m and l.
+    constexpr int OP = DV + 4;
+    float* so = reinterpret_cast<float*>(mine);
+    float* sml = so + NT * 8 * OP;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        const int h = t * 8 + 2 * j + e;
         l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 4);
         l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 8);
         l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 16);
+        if (lane < 4) {
+          sml[2 * h] = m[t][e];
+          sml[2 * h + 1] = l[t][e];
+        }
+#pragma unroll
+        for (int x = 0; x < MT; ++x)
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch)
+            so[h * OP + x * 16 + ch * 8 + (lane >> 2)] = acc[x][t][2 * ch + e];
       }
+    __syncwarp();
+    const int c0 = lane * VPL;
+    const bool in_row = c0 < DV;
     if (n == nb) {
       // the whole unit: finish its rows
+#pragma unroll 1
+      for (int h = 0; h < nh; ++h) {
+        float o[VPL];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int h = t * 8 + 2 * j + e;
-          float f;
-          if (a.no_norm) {
-            f = 1.f / l[t][e];
-          } else {
-            float sq2 = 0.f;
-#pragma unroll
-            for (int x = 0; x < MT; ++x)
-              sq2 += acc[x][t][e] * acc[x][t][e] + acc[x][t][2 + e] * acc[x][t][2 + e];
-            sq2 += __shfl_xor_sync(0xffffffffu, sq2, 4);
-            sq2 += __shfl_xor_sync(0xffffffffu, sq2, 8);
-            sq2 += __shfl_xor_sync(0xffffffffu, sq2, 16);
-            f = 1.f / sqrtf(sq2 / (float)DV + a.eps);
-          }
-          if (h >= nh) continue;
-          const bool none = l[t][e] == 0.f;          // no finite logit
-          const size_t row0 = ((size_t)b * a.Hq + h0 + h) * DV;
-#pragma unroll
-          for (int x = 0; x < MT; ++x)
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-              const int c = x * 16 + ch * 8 + (lane >> 2);
-              float y = acc[x][t][2 * ch + e] * f;
-              if (!a.no_norm) y *= bf2f(a.w[c]);
-              store_y(a, row0 + c, none ? 0.f : y);
-            }
-        }
+        for (int e = 0; e < VPL; ++e) o[e] = 0.f;
+        if (in_row) load_n<VPL>(so + h * OP + c0, o);
+        const float lh = sml[2 * h + 1];
+        const float f = row_factor<VPL>(a, o, lh, DV);
+        if (in_row) store_row<VPL>(a, ((size_t)b * a.Hq + h0 + h) * DV, c0, o, f, lh == 0.f);
+      }
+      if (a.join_by_unit && lane == 0) a.jobs[b * upb + u] = make_int4(0, 0, 0, 0);
     } else {
-      float* slot = a.slots + (2LL * worker + (pos == first ? 0 : 1)) * a.slot_floats;
-      float* sm = slot + a.hpb * DV;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int h = t * 8 + 2 * j + e;
-          if (h >= nh) continue;
-#pragma unroll
-          for (int x = 0; x < MT; ++x)
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch)
-              slot[h * DV + x * 16 + ch * 8 + (lane >> 2)] = acc[x][t][2 * ch + e];
-          if (lane < 4) {
-            sm[h] = m[t][e];
-            sm[a.hpb + h] = l[t][e];
-          }
-        }
-      float* tot = sm + 2 * a.hpb;
-      if constexpr (SCALAR) {
-        if (lane == 0) tot[0] = suf[0][0];
-      } else {
-        if (j == 0) {
-#pragma unroll
-          for (int x = 0; x < MT; ++x)
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) tot[x * 16 + ch * 8 + (lane >> 2)] = suf[x][ch];
+      // slot 1: the unit begins here; slot 0: it began before
+      float* slot = a.slots + (2LL * worker + (t0 == 0)) * a.slot_floats;
+#pragma unroll 1
+      for (int h = 0; h < nh; ++h) {
+        float o[VPL];
+        if (in_row) {
+          load_n<VPL>(so + h * OP + c0, o);
+          store_n<VPL>(slot + h * DV + c0, o);
         }
       }
+      float* tail = slot + a.hpb * DV;
+      if constexpr (SCALAR)
+#pragma unroll
+        for (int e = 1; e < VPL; ++e) suf[e] = suf[0];      // one gate for all channels
+      if (in_row) store_n<VPL>(tail + c0, suf);
+      if (lane < 2 * nh) tail[DV + lane] = sml[lane];
+      if (t0 == 0) {
+        const int wl = (int)((live + nb - 1) / span);
+        job = make_int4(wl - worker + 1, worker, b * upb + u, 0);
+        if (a.join_by_unit && lane == 0) a.jobs[b * upb + u] = job;
+      }
     }
-    pos += n;
+    __syncwarp();
   }
+  if (!a.join_by_unit && lane == 0) a.jobs[worker] = job;
 }
 
 // Joins the pieces of the units that were cut.  grid.x: the units, or (where
 // there are more units than workers) the workers, each for the cut unit that
 // begins in its span; grid.y: the head blocks' heads, heads_per_cta at a time.
 // A head has 8 / heads_per_cta warps, each for a run of its pieces; channels
-// lie over the lanes.  Launched so that it may start while the split kernel
-// still runs: what it reads before the wait are that kernel's inputs.
+// lie over the lanes.  Launched so that its CTAs are in place when the split
+// kernel ends.
 template <int DV, bool SCALAR>
 __global__ void __launch_bounds__(kJoinThreads)
     paged_join_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int VPL = DV >= 32 ? DV / 32 : 1;
   constexpr int kWarps = kJoinThreads / 32;
   __shared__ float so[kWarps][DV], stot[kWarps][DV], sml[kWarps][2];
-  __shared__ int s_unit, s_np, s_w0, s_slot1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int upb = a.Hkv * a.nhb;
-  if (warp == 0) {
-    const long long total = tiles_total(a) * upb;
-    const long long span = (total + a.nworkers - 1) / a.nworkers;
-    int b = 0, u = 0;
-    long long start = 0;
-    int nb = 0;
-    if (a.join_by_unit) {
-      b = blockIdx.x / upb;
-      u = blockIdx.x % upb;
-      nb = paged_tiles(a, b);
-      start = tiles_before(a, b) * upb + (long long)u * nb;
-    } else {
-      const long long e = span * (blockIdx.x + 1);          // where the worker's span ends
-      if (e < total) {
-        long long base;
-        find_tile(a, e, upb, &b, &base);
-        nb = paged_tiles(a, b);
-        u = (int)((e - base) / nb);
-        start = base + (long long)u * nb;
-        if (start == e || start < span * blockIdx.x) nb = 0;   // not cut here, or begun before
-      }
-    }
-    if (lane == 0) {
-      int np = 0, w0 = 0;
-      if (nb > 0) {
-        w0 = (int)(start / span);
-        np = (int)((start + nb - 1) / span) - w0 + 1;
-      }
-      s_np = np;
-      s_w0 = w0;
-      s_unit = b * upb + u;
-      s_slot1 = start != (long long)w0 * span;
-    }
-  }
-  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int np = s_np;
+  const int4 job = a.jobs[blockIdx.x];
+  const int np = job.x;
   if (np < 2) return;
-  const int b = s_unit / upb, u = s_unit % upb;
+  const int b = job.z / upb, u = job.z % upb;
   const int kv = u / a.nhb, hb = u % a.nhb;
   const int nh = min(a.hpb, a.grp - hb * a.hpb);
   const int wph = kWarps / a.heads_per_cta;                 // warps per head
@@ -670,15 +722,16 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (blockIdx.y * a.heads_per_cta >= nh) return;
   const bool live = h < nh && lane * VPL < DV;
   auto slot_of = [&](int i) {
-    return a.slots + (2LL * (s_w0 + i) + (i == 0 ? s_slot1 : 0)) * a.slot_floats;
+    return a.slots + (2LL * (job.y + i) + (i == 0)) * a.slot_floats;
   };
   const int i0 = (int)((long long)np * run / wph), i1 = (int)((long long)np * (run + 1) / wph);
   const int c0 = lane * VPL;
+  const int tail = a.hpb * DV;
   float M = -INFINITY, l = 0.f, o[VPL], after[VPL];
 #pragma unroll
   for (int e = 0; e < VPL; ++e) o[e] = after[e] = 0.f;
   if (h < nh) {
-    for (int i = i0 + lane; i < i1; i += 32) M = fmaxf(M, slot_of(i)[a.hpb * DV + h]);
+    for (int i = i0 + lane; i < i1; i += 32) M = fmaxf(M, slot_of(i)[tail + DV + 2 * h]);
     M = warp_max(M);
   }
   const float ref = M == -INFINITY ? 0.f : M;
@@ -686,20 +739,19 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll 4
     for (int i = i1 - 1; i >= i0; --i) {
       const float* s = slot_of(i);
-      const float f = ex2(s[a.hpb * DV + h] - ref);
-      l += f * s[a.hpb * (DV + 1) + h];
-      const float* tot = s + a.hpb * (DV + 2);
+      const float f = ex2(s[tail + DV + 2 * h] - ref);
+      l += f * s[tail + DV + 2 * h + 1];
+      float x[VPL], t[VPL];
+      load_n<VPL>(s + h * DV + c0, x);
+      load_n<VPL>(s + tail + c0, t);
 #pragma unroll
       for (int e = 0; e < VPL; ++e) {
-        o[e] += f * s[h * DV + c0 + e] * ex2(after[e] * kLog2e);
-        after[e] += SCALAR ? tot[0] : tot[c0 + e];
+        o[e] += f * x[e] * ex2(after[e]);
+        after[e] += t[e];
       }
     }
-#pragma unroll
-    for (int e = 0; e < VPL; ++e) {
-      so[warp][c0 + e] = o[e];
-      stot[warp][c0 + e] = after[e];
-    }
+    store_n<VPL>(&so[warp][c0], o);
+    store_n<VPL>(&stot[warp][c0], after);
     if (lane == 0) {
       sml[warp][0] = M;
       sml[warp][1] = l;
@@ -720,28 +772,13 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (!live) continue;
 #pragma unroll
     for (int e = 0; e < VPL; ++e) {
-      o[e] += f * so[warp + i][c0 + e] * ex2(after[e] * kLog2e);
+      o[e] += f * so[warp + i][c0 + e] * ex2(after[e]);
       after[e] += stot[warp + i][c0 + e];
     }
   }
-  const bool none = l == 0.f;                               // no finite logit
-  float f;
-  if (a.no_norm) {
-    f = 1.f / l;
-  } else {
-    float sq2 = 0.f;
-#pragma unroll
-    for (int e = 0; e < VPL; ++e) sq2 += o[e] * o[e];
-    f = 1.f / sqrtf(warp_sum(sq2) / (float)DV + a.eps);
-  }
-  if (!live) return;
-  const size_t at = ((size_t)b * a.Hq + kv * a.grp + hb * a.hpb + h) * DV + c0;
-#pragma unroll
-  for (int e = 0; e < VPL; ++e) {
-    float y = o[e] * f;
-    if (!a.no_norm) y *= bf2f(a.w[c0 + e]);
-    store_y(a, at + e, none ? 0.f : y);
-  }
+  const float f = row_factor<VPL>(a, o, l, DV);
+  if (live)
+    store_row<VPL>(a, ((size_t)b * a.Hq + kv * a.grp + hb * a.hpb + h) * DV, c0, o, f, l == 0.f);
 }
 
 // ---------------------------------------------------------------- host side
@@ -764,9 +801,9 @@ static int paged_smem_bytes(const Dims& d) {
 }
 
 struct PagedPlan {
-  int nt, hpb, nhb, units, ctas, workers, smem;
+  int nt, hpb, nhb, units, ctas, workers, smem, jobs;
   long long slot_floats;
-  size_t bytes;
+  size_t job_bytes, bytes;
 };
 
 // Grid: as many CTAs as the SMs hold at once (three of them by registers with
@@ -789,7 +826,9 @@ static PagedPlan paged_plan(const Dims& d, const fix_attn_page_cache* c) {
   p.ctas = tiles < (long long)kSMs * per_sm ? (int)tiles : kSMs * per_sm;
   p.workers = p.ctas * kPagedWarps;
   p.slot_floats = ((long long)p.hpb * (d.Dv + 2) + d.Dv + 31) / 32 * 32;
-  p.bytes = (size_t)p.workers * 2 * p.slot_floats * 4;
+  p.jobs = p.units < p.workers ? p.units : p.workers;
+  p.job_bytes = ((size_t)p.jobs * sizeof(int4) + 255) / 256 * 256;
+  p.bytes = p.job_bytes + (size_t)p.workers * 2 * p.slot_floats * 4;
   return p;
 }
 
@@ -808,7 +847,7 @@ static fix_status paged_launch(const PagedArgs& a, const PagedPlan& pl, cudaStre
   kernel<<<pl.ctas, kPagedWarps * 32, pl.smem, st>>>(a);
   FIX_PAGED_TRY(launch_status());
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.join_by_unit ? a.units : a.nworkers,
+  cfg.gridDim = dim3(pl.jobs,
                      (a.hpb + a.heads_per_cta - 1) / a.heads_per_cta);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
@@ -869,12 +908,17 @@ extern "C" fix_status fix_attn_decode_paged(const fix_attn_problem* p, const fix
   a.status = c->status;
   a.nworkers = pl.workers;
   a.slot_floats = pl.slot_floats;
-  a.slots = static_cast<float*>(workspace);
+  a.jobs = static_cast<int4*>(workspace);
+  a.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.job_bytes);
   a.units = pl.units;
-  // few units: a CTA per unit and head, all its warps on the head's pieces;
-  // many: each unit has few pieces, a CTA's warps take a head each
+  // few units: a CTA per unit and head, all its warps on the head's many
+  // pieces; the more units, the fewer pieces each, and the more heads a CTA
+  // takes
   a.join_by_unit = pl.units <= pl.workers;
-  a.heads_per_cta = a.join_by_unit ? 1 : pl.hpb > 4 ? 8 : pl.hpb > 2 ? 4 : pl.hpb;
+  a.heads_per_cta = 1;
+  while (a.heads_per_cta < 8 && a.heads_per_cta < pl.hpb &&
+         pl.jobs * ((pl.hpb + a.heads_per_cta - 1) / a.heads_per_cta) > 2 * kSMs)
+    a.heads_per_cta *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (d.Dv) {
     case 16: return paged_launch_dv<16>(a, pl, d.scalar_gate, st);

@@ -862,3 +862,21 @@ def test_python_refusals_on_the_gpu(cuda_lib):
     with pytest.raises(fixattn.FixStatusError, match="HEAD_DIM"):
         y = torch.zeros(1, 1, 1, 96, dtype=bf16, device="cuda")
         fixattn.fix_attn_rotary(y, y, f)
+
+
+@pytest.mark.gpu
+def test_decode_paged_all_nan(cuda_lib):
+    """NaN in every key, or in one value, of a sequence reaches its rows (as
+    whole rows after the norm), and no other sequence's."""
+    c = Cache([1, 20, 30, 9], 2, 64, 64, 16, seed=3)
+    q, w, _ = decode_inputs(4, 4, 64, 64, 4)
+    c.k[int(c.table[0, 0]), 0] = NAN
+    for i in range(20):
+        c.k[int(c.table[1, i // 16]), i % 16, 1] = NAN            # kv head 1: q heads 2, 3
+    c.v[int(c.table[2, 0]), 5, 0, 7] = NAN                        # kv head 0: q heads 0, 1
+    y = fixattn.fix_attn_decode_paged(q.cuda(), *c.cuda(), w.cuda(), y_dtype=torch.float32).cpu()
+    nan = torch.isnan(y)
+    assert bool(nan[0].all()) and bool(nan[1, 2:].all()) and not nan[1, :2].any()
+    assert bool(nan[2, :2].all()) and not nan[2, 2:].any() and not nan[3].any()
+    check = decode_ref(q[3], *c.tok[3], w, None, 64 ** -0.5, 1e-6, True)
+    assert float((y[3] - check).norm() / check.norm()) <= F32_ROW
