@@ -43,7 +43,7 @@ namespace fix {
 
 constexpr int kTileKeys = 16;
 constexpr int kPagedWarps = 4;         // warps per CTA of the split kernel
-constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = 16;         // at most, per CTA
 constexpr int kSMs = 148;              // B200
 constexpr int kUnitCost = 2;           // line positions of a unit beside its tiles
 
@@ -62,7 +62,7 @@ struct PagedArgs {
   float* slots;                        // two per worker
   int4* jobs;                          // the join's work: (pieces, first worker, unit)
   int units;                           // B * Hkv * nhb
-  int join_by_unit, heads_per_cta;     // shape of the join
+  int join_by_unit, heads_per_cta, warps_per_head;   // shape of the join
 };
 
 __device__ __forceinline__ int paged_len(const PagedArgs& a, int b) {
@@ -699,15 +699,16 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 // Joins the pieces of the units that were cut.  grid.x: the units, or (where
 // there are more units than workers) the workers, each for the cut unit that
 // begins in its span; grid.y: the head blocks' heads, heads_per_cta at a time.
-// A head has 8 / heads_per_cta warps, each for a run of its pieces; channels
-// lie over the lanes.  Launched so that its CTAs are in place when the split
-// kernel ends.
-template <int DV, bool SCALAR>
-__global__ void __launch_bounds__(kJoinThreads)
+// A head has warps_per_head warps, each for a run of its pieces, newest first
+// and four loads deep (what it costs is the latency of its loads); channels
+// lie over the lanes.  Launched so that its CTAs are in place when
+// the split kernel ends.
+template <int DV>
+__global__ void __launch_bounds__(kJoinWarps * 32)
     paged_join_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int VPL = DV >= 32 ? DV / 32 : 1;
-  constexpr int kWarps = kJoinThreads / 32;
-  __shared__ float so[kWarps][DV], stot[kWarps][DV], sml[kWarps][2];
+  constexpr int kDeep = 4;
+  __shared__ float so[kJoinWarps][DV], stot[kJoinWarps][DV], sml[kJoinWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int upb = a.Hkv * a.nhb;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -717,37 +718,50 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int b = job.z / upb, u = job.z % upb;
   const int kv = u / a.nhb, hb = u % a.nhb;
   const int nh = min(a.hpb, a.grp - hb * a.hpb);
-  const int wph = kWarps / a.heads_per_cta;                 // warps per head
+  const int wph = a.warps_per_head;
   const int h = blockIdx.y * a.heads_per_cta + warp / wph, run = warp % wph;
   if (blockIdx.y * a.heads_per_cta >= nh) return;
-  const bool live = h < nh && lane * VPL < DV;
-  auto slot_of = [&](int i) {
-    return a.slots + (2LL * (job.y + i) + (i == 0)) * a.slot_floats;
-  };
-  const int i0 = (int)((long long)np * run / wph), i1 = (int)((long long)np * (run + 1) / wph);
   const int c0 = lane * VPL;
+  const bool live = h < nh && c0 < DV;
+  const int i0 = (int)((long long)np * run / wph), i1 = (int)((long long)np * (run + 1) / wph);
   const int tail = a.hpb * DV;
   float M = -INFINITY, l = 0.f, o[VPL], after[VPL];
 #pragma unroll
   for (int e = 0; e < VPL; ++e) o[e] = after[e] = 0.f;
-  if (h < nh) {
-    for (int i = i0 + lane; i < i1; i += 32) M = fmaxf(M, slot_of(i)[tail + DV + 2 * h]);
-    M = warp_max(M);
-  }
-  const float ref = M == -INFINITY ? 0.f : M;
   if (live) {
-#pragma unroll 4
-    for (int i = i1 - 1; i >= i0; --i) {
-      const float* s = slot_of(i);
-      const float f = ex2(s[tail + DV + 2 * h] - ref);
-      l += f * s[tail + DV + 2 * h + 1];
-      float x[VPL], t[VPL];
-      load_n<VPL>(s + h * DV + c0, x);
-      load_n<VPL>(s + tail + c0, t);
+    for (int i = i1 - 1; i >= i0; i -= kDeep) {
+      float pm[kDeep], pl[kDeep], x[kDeep][VPL], t[kDeep][VPL];
 #pragma unroll
-      for (int e = 0; e < VPL; ++e) {
-        o[e] += f * x[e] * ex2(after[e]);
-        after[e] += t[e];
+      for (int d = 0; d < kDeep; ++d) {
+        // a run's last batch may be short: its missing pieces count nothing
+        const bool there = i - d >= i0;
+        const float* s = a.slots + (2LL * (job.y + i - d) + (i == d)) * a.slot_floats;
+        pm[d] = there ? s[tail + DV + 2 * h] : -INFINITY;
+        pl[d] = there ? s[tail + DV + 2 * h + 1] : 0.f;
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) x[d][e] = t[d][e] = 0.f;
+        if (there) {
+          load_n<VPL>(s + h * DV + c0, x[d]);
+          load_n<VPL>(s + tail + c0, t[d]);
+        }
+      }
+      float mx = M;
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) mx = fmaxf(mx, pm[d]);
+      const float ref = mx == -INFINITY ? 0.f : mx, f0 = ex2(M - ref);
+      M = mx;
+      l *= f0;
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) o[e] *= f0;
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) {
+        const float f = ex2(pm[d] - ref);
+        l += f * pl[d];
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) {
+          o[e] += f * x[d][e] * ex2(after[e]);
+          after[e] += t[d][e];
+        }
       }
     }
     store_n<VPL>(&so[warp][c0], o);
@@ -766,6 +780,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   l = 0.f;
 #pragma unroll
   for (int e = 0; e < VPL; ++e) o[e] = after[e] = 0.f;
+#pragma unroll 4
   for (int i = wph - 1; i >= 0; --i) {
     const float f = ex2(sml[warp + i][0] - M);
     l += f * sml[warp + i][1];
@@ -849,14 +864,14 @@ static fix_status paged_launch(const PagedArgs& a, const PagedPlan& pl, cudaStre
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(pl.jobs,
                      (a.hpb + a.heads_per_cta - 1) / a.heads_per_cta);
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.blockDim = dim3(a.heads_per_cta * a.warps_per_head * 32);
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, paged_join_kernel<DV, SCALAR>, a);
+  cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, a);
   return launch_status();
 }
 
@@ -911,14 +926,17 @@ extern "C" fix_status fix_attn_decode_paged(const fix_attn_problem* p, const fix
   a.jobs = static_cast<int4*>(workspace);
   a.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.job_bytes);
   a.units = pl.units;
-  // few units: a CTA per unit and head, all its warps on the head's many
-  // pieces; the more units, the fewer pieces each, and the more heads a CTA
-  // takes
+  // warps per head: about one per piece that a unit of average length has, up
+  // to some 4096 in all (28 per SM); CTAs of four warps at least
   a.join_by_unit = pl.units <= pl.workers;
+  const int pieces = pl.workers / pl.jobs;
+  const long long rows = (long long)pl.jobs * pl.hpb;
+  a.warps_per_head = 1;
+  while (a.warps_per_head < kJoinWarps && 2 * a.warps_per_head <= pieces &&
+         rows * 2 * a.warps_per_head <= 4096)
+    a.warps_per_head *= 2;
   a.heads_per_cta = 1;
-  while (a.heads_per_cta < 8 && a.heads_per_cta < pl.hpb &&
-         pl.jobs * ((pl.hpb + a.heads_per_cta - 1) / a.heads_per_cta) > 2 * kSMs)
-    a.heads_per_cta *= 2;
+  while (a.heads_per_cta * a.warps_per_head < 4 && a.heads_per_cta < pl.hpb) a.heads_per_cta *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (d.Dv) {
     case 16: return paged_launch_dv<16>(a, pl, d.scalar_gate, st);

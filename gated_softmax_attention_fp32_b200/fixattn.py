@@ -310,23 +310,34 @@ def fix_attn_decode(q, k_cache, v_cache, g_cache, seqlens, o_norm_weight=None, s
     return y
 
 
+# The checks below run on every call of a decode step, whose kernels take a
+# few microseconds: they ask a tensor for no more than they need (dtype and
+# device index by identity and number, not torch.device objects).
+_Tensor = torch.Tensor
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
-def _tensor(name, t, dtype, device):
-    """A tensor argument of the right type on the call's GPU."""
-    if not isinstance(t, torch.Tensor):
+def _bad_tensor(name, t, dtype, index):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
-def _dense(name, t, dtype, device, shape):
-    _tensor(name, t, dtype, device)
+def _tensor(name, t, dtype, index):
+    """A tensor argument of the right type on the call's GPU."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != index:
+        _bad_tensor(name, t, dtype, index)
+
+
+def _dense(name, t, dtype, index, shape):
+    _tensor(name, t, dtype, index)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
@@ -351,52 +362,81 @@ def _token_stride(name, t, inner):
     return s
 
 
-def _cuda_device(name, t):
-    if not isinstance(t, torch.Tensor):
+def _cuda_index(name, t):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.device.type != "cuda":
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
-    return t.device
+    return index
 
 
-class _on:
-    """Makes ``device`` current, and ``stream`` where one is given, so that
-    what is allocated meanwhile belongs to the stream that uses it.  Costs
-    nothing where both are current already."""
+class _On:
+    """Makes device ``index`` current, and ``stream`` where one is given, so
+    that what is allocated meanwhile belongs to the stream that uses it;
+    yields the stream's handle."""
 
-    def __init__(self, device, stream):
-        self.ctx = []
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-            self.ctx.append(torch.cuda.stream(stream))     # sets the device too
-        elif torch.cuda.current_device() != device.index:
-            self.ctx.append(torch.cuda.device(device))
+    def __init__(self, index, stream):
+        self.index = index
+        if stream is None:
+            self.ctx = torch.cuda.device(index)
+        else:
+            _need(stream.device.index == index,
+                  f"the stream is on {stream.device}, the tensors on cuda:{index}")
+            self.ctx = torch.cuda.stream(stream)           # sets the device too
 
     def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        self.ctx.__enter__()
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
-        for c in self.ctx:
-            c.__exit__(*exc)
+        self.ctx.__exit__(*exc)
 
 
-def _rotation(inv_freq, Dk, interleaved, device):
-    _tensor("inv_freq", inv_freq, torch.float32, device)
+class _Here:
+    """The device and its current stream, both as they are already."""
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        return _raw_stream(self.index)
+
+    def __exit__(self, *exc):
+        pass
+
+
+_here = {}
+
+
+def _on(index, stream):
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return _here.get(index) or _here.setdefault(index, _Here(index))
+    return _On(index, stream)
+
+
+def _empty(shape, dtype, index):
+    return torch.empty(shape, dtype=dtype, device=_devices.get(index) or
+                       _devices.setdefault(index, torch.device("cuda", index)))
+
+
+_devices = {}
+
+
+def _rotation(inv_freq, Dk, interleaved, index):
+    _tensor("inv_freq", inv_freq, torch.float32, index)
     _need(inv_freq.dim() == 1 and inv_freq.is_contiguous(), "inv_freq must be a dense vector")
     rot = 2 * inv_freq.numel()
-    _need(rot % 16 == 0 and 16 <= rot <= Dk,
-          f"inv_freq must hold rot_dim/2 frequencies, rot_dim a multiple of 16 in [16, {Dk}]")
-    return Rotation(inv_freq.data_ptr(), rot, int(bool(interleaved)))
+    if rot % 16 or rot < 16 or rot > Dk:
+        raise ValueError("inv_freq must hold rot_dim/2 frequencies, rot_dim a multiple of 16 in "
+                         f"[16, {Dk}]")
+    return Rotation(inv_freq.data_ptr(), rot, 1 if interleaved else 0)
 
 
-def _token_problem(q_heads, k_heads, B, T, Dk, Dv, cu_seqlens, device, scalar=False):
-    p = Problem(batch=B, seqlen=T, num_q_heads=q_heads, num_kv_heads=k_heads, head_dim_k=Dk,
-                head_dim_v=Dv, flags=FIX_FLAG_SCALAR_GATE if scalar else 0)
+def _token_problem(q_heads, k_heads, B, T, Dk, Dv, cu_seqlens, index, scalar=False):
+    p = Problem(B, T, q_heads, k_heads, Dk, Dv, 0, 0, 0, FIX_FLAG_SCALAR_GATE if scalar else 0)
     if cu_seqlens is not None:
-        _tensor("cu_seqlens", cu_seqlens, torch.int64, device)
+        _tensor("cu_seqlens", cu_seqlens, torch.int64, index)
         _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2 and cu_seqlens.is_contiguous(),
               "cu_seqlens must be a dense int64 vector of S + 1 entries")
         _need(B == 1, "packed sequences use a batch of 1")
@@ -416,62 +456,69 @@ def fix_attn_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved
     or int32 ``positions`` [B,T].  q and k may be views of one projection's
     output.  ``inverse`` turns back (the gradient).  Returns new dense (q, k),
     or ``out`` = (q_out, k_out), which may be dense inputs themselves."""
-    dev = _cuda_device("q", q)
-    _tensor("q", q, torch.bfloat16, dev)
+    index = _cuda_index("q", q)
+    _tensor("q", q, torch.bfloat16, index)
     _need(q.dim() == 4, "q must be [B,T,Hq,Dk]")
     B, T, Hq, Dk = q.shape
-    Hkv = Hq
+    Hkv, ks, kp = Hq, 0, None
     if k is not None:
-        _tensor("k", k, torch.bfloat16, dev)
-        _need(k.dim() == 4 and k.shape[:2] == q.shape[:2] and k.shape[3] == Dk,
-              "k must be [B,T,Hkv,Dk] with q's B, T and Dk")
-        Hkv = k.shape[2]
-    r = _rotation(inv_freq, Dk, interleaved, dev)
-    p = _token_problem(Hq, Hkv, B, T, Dk, Dk, cu_seqlens, dev)
+        _tensor("k", k, torch.bfloat16, index)
+        _need(k.dim() == 4, "k must be [B,T,Hkv,Dk]")
+        Bk, Tk, Hkv, Dkk = k.shape
+        _need(Bk == B and Tk == T and Dkk == Dk, "k must have q's B, T and Dk")
+        ks = _token_stride("k", k, Hkv * Dk)
+        kp = k.data_ptr()
+    r = _rotation(inv_freq, Dk, interleaved, index)
+    p = _token_problem(Hq, Hkv, B, T, Dk, Dk, cu_seqlens, index)
     if positions is not None:
-        _dense("positions", positions, torch.int32, dev, q.shape[:2])
+        _dense("positions", positions, torch.int32, index, (B, T))
     qs = _token_stride("q", q, Hq * Dk)
-    ks = _token_stride("k", k, Hkv * Dk) if k is not None else 0
-    with _on(dev, stream) as st:
+    with _on(index, stream) as st:
         if out is None:
-            q_out = torch.empty((B, T, Hq, Dk), dtype=torch.bfloat16, device=dev)
-            k_out = (torch.empty((B, T, Hkv, Dk), dtype=torch.bfloat16, device=dev)
-                     if k is not None else None)
+            q_out = _empty((B, T, Hq, Dk), torch.bfloat16, index)
+            k_out = _empty((B, T, Hkv, Dk), torch.bfloat16, index) if k is not None else None
         else:
             q_out, k_out = out
-            _dense("out[0]", q_out, torch.bfloat16, dev, q.shape)
+            _dense("out[0]", q_out, torch.bfloat16, index, (B, T, Hq, Dk))
             _need((k is None) == (k_out is None), "out[1] goes with k")
             if k is not None:
-                _dense("out[1]", k_out, torch.bfloat16, dev, k.shape)
-        s = load().fix_attn_rotary(ctypes.byref(p), ctypes.byref(r), _ptr(positions), _ptr(q), qs,
-                                   _ptr(k), ks, _ptr(q_out), _ptr(k_out), int(bool(inverse)), st)
+                _dense("out[1]", k_out, torch.bfloat16, index, (B, T, Hkv, Dk))
+        s = load().fix_attn_rotary(
+            p, r, None if positions is None else positions.data_ptr(), q.data_ptr(), qs, kp, ks,
+            q_out.data_ptr(), None if k is None else k_out.data_ptr(), 1 if inverse else 0, st)
     if s != 0:
         raise FixStatusError(s, "fix_attn_rotary")
     return q_out, k_out
 
 
-def _page_cache(k_pages, v_pages, g_pages, page_table, seqlens, status, S, dev):
-    _tensor("k_pages", k_pages, torch.bfloat16, dev)
-    _need(k_pages.dim() == 4 and k_pages.is_contiguous(),
+def _page_cache(k_pages, v_pages, g_pages, page_table, seqlens, status, S, index):
+    """(PageCache, Hkv, Dk, Dv, scalar gate)."""
+    _tensor("k_pages", k_pages, torch.bfloat16, index)
+    _tensor("v_pages", v_pages, torch.bfloat16, index)
+    _tensor("g_pages", g_pages, torch.float32, index)
+    _tensor("page_table", page_table, torch.int32, index)
+    _tensor("seqlens", seqlens, torch.int32, index)
+    kd, vd, gd = k_pages.shape, v_pages.shape, g_pages.shape
+    _need(len(kd) == 4 and k_pages.is_contiguous(),
           "k_pages must be a dense [num_pages,page_size,Hkv,Dk]")
-    P, ps, Hkv, _ = k_pages.shape
-    _tensor("v_pages", v_pages, torch.bfloat16, dev)
-    _need(v_pages.dim() == 4 and v_pages.is_contiguous() and v_pages.shape[:3] == k_pages.shape[:3],
+    _need(len(vd) == 4 and vd[:3] == kd[:3] and v_pages.is_contiguous(),
           "v_pages must be a dense [num_pages,page_size,Hkv,Dv]")
-    _tensor("g_pages", g_pages, torch.float32, dev)
-    _need(g_pages.is_contiguous() and (g_pages.shape == v_pages.shape
-                                       or g_pages.shape == v_pages.shape[:3]),
+    scalar = len(gd) == 3
+    _need(gd == (vd[:3] if scalar else vd) and g_pages.is_contiguous(),
           "g_pages must be a dense [num_pages,page_size,Hkv,Dv] or [num_pages,page_size,Hkv]")
-    _tensor("page_table", page_table, torch.int32, dev)
-    _need(page_table.dim() == 2 and page_table.is_contiguous() and page_table.shape[0] == S,
-          f"page_table must be a dense [{S},max_pages]")
-    _dense("seqlens", seqlens, torch.int32, dev, (S,))
+    td = page_table.shape
+    if len(td) != 2 or td[0] != S or not page_table.is_contiguous():
+        raise ValueError(f"page_table must be a dense [{S},max_pages]")
+    if seqlens.shape != (S,) or not seqlens.is_contiguous():
+        raise ValueError(f"seqlens must be a dense [{S}]")
+    sp = None
     if status is not None:
-        _tensor("status", status, torch.int32, dev)
+        _tensor("status", status, torch.int32, index)
         _need(status.numel() == 1, "status must hold one int32")
-    return PageCache(ps, P, page_table.shape[1], page_table.data_ptr(), seqlens.data_ptr(),
-                     k_pages.data_ptr(), v_pages.data_ptr(), g_pages.data_ptr(),
-                     status.data_ptr() if status is not None else None)
+        sp = status.data_ptr()
+    return (PageCache(kd[1], kd[0], td[1], page_table.data_ptr(), seqlens.data_ptr(),
+                      k_pages.data_ptr(), v_pages.data_ptr(), g_pages.data_ptr(), sp),
+            kd[2], kd[3], vd[3], scalar)
 
 
 def fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlens,
@@ -487,43 +534,43 @@ def fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlen
     Tokens at negative positions are padding and not stored.  Returns (q, k)
     rotated: None without ``q`` / unless ``return_k``.  ``status`` (int32 [1])
     is set to FIX_ERR_PAGE if a token had no page (it is skipped)."""
-    dev = _cuda_device("k", k)
-    _tensor("k", k, torch.bfloat16, dev)
-    _tensor("v", v, torch.bfloat16, dev)
-    _tensor("g", g, torch.float32, dev)
-    _need(k.dim() == 4 and v.dim() == 4 and v.shape[:3] == k.shape[:3],
+    index = _cuda_index("k", k)
+    _tensor("k", k, torch.bfloat16, index)
+    _tensor("v", v, torch.bfloat16, index)
+    _tensor("g", g, torch.float32, index)
+    kd, vd, gd = k.shape, v.shape, g.shape
+    _need(len(kd) == 4 and len(vd) == 4 and vd[:3] == kd[:3],
           "k and v must be [B,T,Hkv,Dk] and [B,T,Hkv,Dv]")
-    B, T, Hkv, Dk = k.shape
-    Dv = v.shape[3]
-    scalar = g.dim() == 3
-    _need(g.shape == (v.shape[:3] if scalar else v.shape),
-          "g must be [B,T,Hkv,Dv] or [B,T,Hkv]")
-    Hq = Hkv
+    B, T, Hkv, Dk = kd
+    Dv = vd[3]
+    scalar = len(gd) == 3
+    _need(gd == (vd[:3] if scalar else vd), "g must be [B,T,Hkv,Dv] or [B,T,Hkv]")
+    Hq, qs, qp = Hkv, 0, None
     if q is not None:
-        _tensor("q", q, torch.bfloat16, dev)
-        _need(q.dim() == 4 and q.shape[:2] == k.shape[:2] and q.shape[3] == Dk,
-              "q must be [B,T,Hq,Dk] with k's B, T and Dk")
-        Hq = q.shape[2]
+        _tensor("q", q, torch.bfloat16, index)
+        _need(q.dim() == 4, "q must be [B,T,Hq,Dk]")
+        Bq, Tq, Hq, Dkq = q.shape
+        _need(Bq == B and Tq == T and Dkq == Dk, "q must have k's B, T and Dk")
+        qs = _token_stride("q", q, Hq * Dk)
+        qp = q.data_ptr()
     _need(inv_freq is not None or (q is None and not return_k),
           "q and return_k go with inv_freq")
-    p = _token_problem(Hq, Hkv, B, T, Dk, Dv, cu_seqlens, dev, scalar)
-    c = _page_cache(k_pages, v_pages, g_pages, page_table, seqlens, status,
-                    p.num_seqs if cu_seqlens is not None else B, dev)
-    _need(k_pages.shape[2:] == k.shape[2:] and v_pages.shape[3] == Dv
-          and (g_pages.dim() == 3) == scalar, "the pages must have the tokens' heads, dims and gate")
-    r = _rotation(inv_freq, Dk, interleaved, dev) if inv_freq is not None else None
-    qs = _token_stride("q", q, Hq * Dk) if q is not None else 0
+    p = _token_problem(Hq, Hkv, B, T, Dk, Dv, cu_seqlens, index, scalar)
+    c, Hp, Dkp, Dvp, sp = _page_cache(k_pages, v_pages, g_pages, page_table, seqlens, status,
+                                      p.num_seqs if cu_seqlens is not None else B, index)
+    _need(Hp == Hkv and Dkp == Dk and Dvp == Dv and sp == scalar,
+          "the pages must have the tokens' heads, dims and gate")
+    r = _rotation(inv_freq, Dk, interleaved, index) if inv_freq is not None else None
     ks = _token_stride("k", k, Hkv * Dk)
     vs = _token_stride("v", v, Hkv * Dv)
     gs = _token_stride("g", g, Hkv if scalar else Hkv * Dv)
-    with _on(dev, stream) as st:
-        q_out = (torch.empty((B, T, Hq, Dk), dtype=torch.bfloat16, device=dev)
-                 if q is not None else None)
-        k_out = (torch.empty((B, T, Hkv, Dk), dtype=torch.bfloat16, device=dev)
-                 if return_k else None)
+    with _on(index, stream) as st:
+        q_out = _empty((B, T, Hq, Dk), torch.bfloat16, index) if q is not None else None
+        k_out = _empty((B, T, Hkv, Dk), torch.bfloat16, index) if return_k else None
         s = load().fix_attn_append_paged(
-            ctypes.byref(p), ctypes.byref(c), ctypes.byref(r) if r is not None else None, _ptr(q),
-            qs, _ptr(k), ks, _ptr(v), vs, _ptr(g), gs, _ptr(q_out), _ptr(k_out), st)
+            p, c, r, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), gs,
+            None if q_out is None else q_out.data_ptr(),
+            None if k_out is None else k_out.data_ptr(), st)
     if s != 0:
         raise FixStatusError(s, "fix_attn_append_paged")
     return q_out, k_out
@@ -531,28 +578,28 @@ def fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlen
 
 def _paged_problem(q, k_pages, v_pages, g_pages, page_table, seqlens, scale, eps, y_dtype, o_norm,
                    status):
-    dev = _cuda_device("q", q)
-    _tensor("q", q, torch.bfloat16, dev)
+    index = _cuda_index("q", q)
+    _tensor("q", q, torch.bfloat16, index)
     _need(q.dim() == 3 and q.is_contiguous(), "q must be a dense [B,Hq,Dk]")
-    _need(y_dtype in (torch.bfloat16, torch.float32), "y_dtype must be bfloat16 or float32")
+    _need(y_dtype is torch.bfloat16 or y_dtype is torch.float32,
+          "y_dtype must be bfloat16 or float32")
     B, Hq, Dk = q.shape
-    c = _page_cache(k_pages, v_pages, g_pages, page_table, seqlens, status, B, dev)
-    _need(k_pages.shape[3] == Dk, "q must have the pages' Dk")
-    p = Problem(batch=B, seqlen=1, num_q_heads=Hq, num_kv_heads=k_pages.shape[2], head_dim_k=Dk,
-                head_dim_v=v_pages.shape[3], y_dtype=1 if y_dtype == torch.float32 else 0,
-                flags=(0 if o_norm else FIX_FLAG_NO_NORM)
-                | (FIX_FLAG_SCALAR_GATE if g_pages.dim() == 3 else 0),
-                scale=float(scale) if scale is not None else 0.0, eps=float(eps))
-    return dev, p, c
+    c, Hkv, Dkp, Dv, scalar = _page_cache(k_pages, v_pages, g_pages, page_table, seqlens, status,
+                                          B, index)
+    _need(Dkp == Dk, "q must have the pages' Dk")
+    p = Problem(B, 1, Hq, Hkv, Dk, Dv, 0, 1 if y_dtype is torch.float32 else 0, 0,
+                (0 if o_norm else FIX_FLAG_NO_NORM) | (FIX_FLAG_SCALAR_GATE if scalar else 0),
+                None, None, 0.0 if scale is None else scale, eps)
+    return index, p, c, (B, Hq, Dv)
 
 
 def fix_attn_decode_paged_workspace(q, k_pages, v_pages, g_pages, page_table, seqlens):
     """A workspace for ``fix_attn_decode_paged`` calls of this shape that do
     not overlap (uint8 tensor; needs no initialisation)."""
-    dev, p, c = _paged_problem(q, k_pages, v_pages, g_pages, page_table, seqlens, None, 1e-6,
-                               torch.bfloat16, True, None)
-    n = int(load().fix_attn_decode_paged_workspace_bytes(ctypes.byref(p), ctypes.byref(c)))
-    return torch.empty(max(n, 1), device=dev, dtype=torch.uint8)
+    index, p, c, _ = _paged_problem(q, k_pages, v_pages, g_pages, page_table, seqlens, None, 1e-6,
+                                    torch.bfloat16, True, None)
+    return _empty(max(int(load().fix_attn_decode_paged_workspace_bytes(p, c)), 1), torch.uint8,
+                  index)
 
 
 def fix_attn_decode_paged(q, k_pages, v_pages, g_pages, page_table, seqlens, o_norm_weight=None,
@@ -564,31 +611,30 @@ def fix_attn_decode_paged(q, k_pages, v_pages, g_pages, page_table, seqlens, o_n
     contiguous cache.  int32 ``seqlens`` [B] on the device; length 0 gives 0.
     ``status`` (int32 [1]) is set to FIX_ERR_PAGE if a token had no page (it
     is left out).  Returns y [B,Hq,Dv]."""
-    dev, p, c = _paged_problem(q, k_pages, v_pages, g_pages, page_table, seqlens, scale, eps,
-                               y_dtype, o_norm, status)
-    B, Hq, Dv = p.batch, p.num_q_heads, p.head_dim_v
-    if o_norm:
-        _need(o_norm_weight is not None, "o_norm=True needs o_norm_weight")
+    index, p, c, shape = _paged_problem(q, k_pages, v_pages, g_pages, page_table, seqlens, scale,
+                                        eps, y_dtype, o_norm, status)
+    _need(o_norm_weight is not None or not o_norm, "o_norm=True needs o_norm_weight")
+    wp = zp = None
     if o_norm_weight is not None:
-        _dense("o_norm_weight", o_norm_weight, torch.bfloat16, dev, (Dv,))
+        _dense("o_norm_weight", o_norm_weight, torch.bfloat16, index, shape[2:])
+        wp = o_norm_weight.data_ptr()
     if o_gate is not None:
-        _dense("o_gate", o_gate, torch.bfloat16, dev, (B, Hq, Dv))
+        _dense("o_gate", o_gate, torch.bfloat16, index, shape)
+        zp = o_gate.data_ptr()
     lib = load()
-    with _on(dev, stream) as st:
+    with _on(index, stream) as st:
         if out is None:
-            out = torch.empty((B, Hq, Dv), device=dev, dtype=y_dtype)
+            out = _empty(shape, y_dtype, index)
         else:
-            _dense("out", out, y_dtype, dev, (B, Hq, Dv))
+            _dense("out", out, y_dtype, index, shape)
         if workspace is None:
-            nbytes = int(lib.fix_attn_decode_paged_workspace_bytes(ctypes.byref(p),
-                                                                   ctypes.byref(c)))
-            workspace = torch.empty(max(nbytes, 1), device=dev, dtype=torch.uint8)
+            workspace = _empty(max(lib.fix_attn_decode_paged_workspace_bytes(p, c), 1),
+                               torch.uint8, index)
         else:
-            _tensor("workspace", workspace, torch.uint8, dev)
+            _tensor("workspace", workspace, torch.uint8, index)
             _need(workspace.is_contiguous(), "workspace must be contiguous")
-        s = lib.fix_attn_decode_paged(ctypes.byref(p), ctypes.byref(c), _ptr(q),
-                                      _ptr(o_norm_weight), _ptr(o_gate), _ptr(out),
-                                      _ptr(workspace), workspace.numel(), st)
+        s = lib.fix_attn_decode_paged(p, c, q.data_ptr(), wp, zp, out.data_ptr(),
+                                      workspace.data_ptr(), workspace.numel(), st)
     if s != 0:
         raise FixStatusError(s, "fix_attn_decode_paged")
     return out
@@ -648,8 +694,8 @@ class _FixRotary(torch.autograd.Function):
     def backward(ctx, dq, dk):
         # the rotation is linear and orthogonal: its gradient is the rotation
         # back, itself differentiable
-        dq, dk = _FixRotary.apply(dq.contiguous(), dk.contiguous(), *ctx.saved_tensors,
-                                  *ctx.cfg)
+        apply = _FixRotary.apply if torch.is_grad_enabled() else fix_attn_rotary
+        dq, dk = apply(dq.contiguous(), dk.contiguous(), *ctx.saved_tensors, *ctx.cfg)
         return dq, dk, None, None, None, None, None
 
 
