@@ -6,10 +6,13 @@
 // there, so that positions of any size keep an angle error near 1e-7; the
 // products and sums are float, rounded to bf16 once.
 //
-// Memory bound: a token's heads are read once and written once.  One CTA per
-// token computes the token's rot_dim/2 sines and cosines into shared memory
-// once, for all its heads; a thread then moves 16 channels of a head (two
-// 16-byte loads and stores): the 8 + 8 channels that eight pairs span.
+// Memory bound: a token's heads are read once and written once.  A token is a
+// list of 32-byte units: eight pairs of a rotated head (8 + 8 channels), or 32
+// consecutive bytes that are copied.  A warp takes up to kItems units per lane
+// of one token, and works alone: it issues all its loads first, then finds the
+// token's position, then the sines and cosines (two angles per lane, shared
+// within the warp; a lane's units all have the same pairs, as the units of a
+// head divide 32), then rotates and stores.
 #include "fix_internal.h"
 
 #define FIX_ROT_TRY(expr)             \
@@ -20,10 +23,10 @@
 
 namespace fix {
 
-constexpr int kTokThreads = 128;
+constexpr int kTokWarps = 4;      // warps per CTA: four tokens
 
 struct TokenArgs {
-  long long N;                    // tokens
+  int N;                          // tokens
   int T;                          // tokens per sequence when not packed
   int nseq;
   const int64_t* cu;              // packed lengths or NULL
@@ -36,6 +39,8 @@ struct TokenArgs {
   const float* g;
   long long qs, ks, vs, gs;       // elements between tokens
   __nv_bfloat16 *q_out, *k_out;
+  int nq, nk, nv, ng;             // units of a token's q, k, v, g
+  int items;                      // units per lane of a warp
   // paged cache (append only)
   const int* table;
   int page_size, num_pages, max_pages;
@@ -51,134 +56,156 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
-// Sequence b of token n and its index in it; false behind the last sequence.
-__device__ __forceinline__ bool find_seq(const TokenArgs& a, long long n, int* b, long long* t,
+// Sequence b of token n and its index in it; false behind the last sequence
+// (whole warp).
+__device__ __forceinline__ bool find_seq(const TokenArgs& a, int n, int* b, long long* t,
                                          long long* len) {
   if (!a.cu) {
-    *b = (int)(n / a.T);
-    *t = n - (long long)*b * a.T;
+    *b = n / a.T;
+    *t = n - *b * a.T;
     *len = a.T;
     return true;
   }
-  int lo = 0, hi = a.nseq;            // the first b with cu[b + 1] > n
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu[mid + 1] > n) hi = mid; else lo = mid + 1;
+  // how many sequences end at or before n: 32 probes a round
+  const int lane = threadIdx.x & 31;
+  int base = 0, left = a.nseq;
+  while (left > 0) {
+    const int step = (left + 31) / 32, at = (lane + 1) * step - 1;
+    const bool before = at < left && a.cu[base + at + 1] <= n;
+    const int skip = __popc(__ballot_sync(0xffffffffu, before)) * step;
+    base += skip;
+    left = min(step - 1, left - skip);
   }
-  if (lo >= a.nseq) return false;
-  *b = lo;
-  *t = n - a.cu[lo];
-  *len = a.cu[lo + 1] - a.cu[lo];
+  if (base >= a.nseq) return false;
+  *b = base;
+  *t = n - a.cu[base];
+  *len = a.cu[base + 1] - a.cu[base];
   return *t >= 0;
 }
 
-// Rotates (or, with cs == NULL, copies) the 16 channels of unit u of one head
-// row and stores them to dst and, where given, dst2.
-__device__ __forceinline__ void rotate_unit(const TokenArgs& a, const float2* cs, int u,
-                                            const __nv_bfloat16* src, __nv_bfloat16* dst,
-                                            __nv_bfloat16* dst2) {
-  const bool turn = u * 16 < a.rot;
-  const int e0 = (turn && !a.interleaved) ? 8 * u : 16 * u;
-  const int e1 = (turn && !a.interleaved) ? a.rot / 2 + 8 * u : 16 * u + 8;
-  uint4 x = *reinterpret_cast<const uint4*>(src + e0);
-  uint4 y = *reinterpret_cast<const uint4*>(src + e1);
-  if (turn && cs) {
-    uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
-    uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
-    const float2* f = cs + 8 * u;
-    if (!a.interleaved) {
+// Rotates the eight pairs of a unit in place.
+__device__ __forceinline__ void rotate_pairs(uint4& x, uint4& y, const float2* f, int interleaved) {
+  uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+  uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
+  if (!interleaved) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 c0 = f[2 * i], c1 = f[2 * i + 1];
-        const float a0 = lo_f(xw[i]), a1 = hi_f(xw[i]), b0 = lo_f(yw[i]), b1 = hi_f(yw[i]);
-        xw[i] = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
-        yw[i] = pack_bf16(a0 * c0.y + b0 * c0.x, a1 * c1.y + b1 * c1.x);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 c0 = f[i], c1 = f[4 + i];
-        const float a0 = lo_f(xw[i]), b0 = hi_f(xw[i]), a1 = lo_f(yw[i]), b1 = hi_f(yw[i]);
-        xw[i] = pack_bf16(a0 * c0.x - b0 * c0.y, a0 * c0.y + b0 * c0.x);
-        yw[i] = pack_bf16(a1 * c1.x - b1 * c1.y, a1 * c1.y + b1 * c1.x);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float2 c0 = f[2 * i], c1 = f[2 * i + 1];
+      const float a0 = lo_f(xw[i]), a1 = hi_f(xw[i]), b0 = lo_f(yw[i]), b1 = hi_f(yw[i]);
+      xw[i] = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
+      yw[i] = pack_bf16(a0 * c0.y + b0 * c0.x, a1 * c1.y + b1 * c1.x);
     }
-  }
-  if (dst) {
-    *reinterpret_cast<uint4*>(dst + e0) = x;
-    *reinterpret_cast<uint4*>(dst + e1) = y;
-  }
-  if (dst2) {
-    *reinterpret_cast<uint4*>(dst2 + e0) = x;
-    *reinterpret_cast<uint4*>(dst2 + e1) = y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 c0 = f[i], c1 = f[4 + i];
+      const float a0 = lo_f(xw[i]), b0 = hi_f(xw[i]), a1 = lo_f(yw[i]), b1 = hi_f(yw[i]);
+      xw[i] = pack_bf16(a0 * c0.x - b0 * c0.y, a0 * c0.y + b0 * c0.x);
+      yw[i] = pack_bf16(a1 * c1.x - b1 * c1.y, a1 * c1.y + b1 * c1.x);
+    }
   }
 }
 
-// grid N, block kTokThreads
-__global__ void __launch_bounds__(kTokThreads) token_kernel(TokenArgs a) {
-  __shared__ float2 cs[64];
-  __shared__ long long s_pos, s_row;
-  const int tid = threadIdx.x;
-  const long long n = blockIdx.x;
-  if (tid == 0) {
-    int b = 0;
-    long long t = 0, len = 0, pos = -1, row = -1;
-    if (a.positions) {
-      pos = a.positions[n];
-    } else if (find_seq(a, n, &b, &t, &len)) {
-      pos = a.seqlens ? (long long)a.seqlens[b] - len + t : t;
-      if (a.seqlens && pos >= 0) {
-        const long long col = pos / a.page_size;
-        int page = -1;
-        if (col < a.max_pages) page = a.table[(long long)b * a.max_pages + col];
-        if (page >= 0 && page < a.num_pages)
-          row = (long long)page * a.page_size + pos % a.page_size;
-        else if (a.status)
-          *a.status = FIX_ERR_PAGE;
-      }
+// grid (tokens / 4, runs of 32 a.items units), a warp per token and run
+template <int kItems>
+__global__ void __launch_bounds__(kTokWarps * 32) token_kernel(const __grid_constant__ TokenArgs a) {
+  __shared__ float4 cs[kTokWarps][4][8];        // (cos, sin) of pairs 8 u + 2 i, + 1 at [i][u]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = blockIdx.x * kTokWarps + warp;
+  if (n >= a.N) return;
+  const int uk = a.Dk / 16, u = lane & (uk - 1);
+  const int first = blockIdx.y * a.items * 32 + lane;
+  const int qk = a.nq + a.nk, qkv = qk + a.nv, all = qkv + a.ng;
+  const bool turning = u * 16 < a.rot;
+  // Unit id of a token's q starts 32 (id - u) bytes into it, at its head's
+  // row, and has its halves e0 and e1 bytes into the row; likewise k.  Units
+  // of v and g are 32 bytes after one another.
+  const bool apart = turning && !a.interleaved;
+  const long long e0 = apart ? -16 * u : 0, step = apart ? a.rot : 16;
+  auto unit_of = [&](const void* q, const void* k, const void* v, const void* g, int id) {
+    const char* p = static_cast<const char*>(id < a.nq ? q : id < qk ? k : id < qkv ? v : g);
+    const int from = id < a.nq ? 0 : id < qk ? a.nq : id < qkv ? qk : qkv;
+    return p + (id < qk ? e0 : 0) + (long long)(id - from) * 32;
+  };
+
+  uint4 x[kItems], y[kItems];
+  const void *qs = a.q + n * a.qs, *ks = a.k + n * a.ks, *vs = a.v + n * a.vs, *gs = a.g + n * a.gs;
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int id = first + i * 32;
+    if (i < a.items && id < all) {
+      const char* p = unit_of(qs, ks, vs, gs, id);
+      x[i] = *reinterpret_cast<const uint4*>(p);
+      y[i] = *reinterpret_cast<const uint4*>(p + (id < qk ? step : 16));
     }
-    s_pos = pos;
-    s_row = row;
   }
-  __syncthreads();
-  const long long pos = s_pos, row = s_row;
-  const bool turn = a.rot && (pos >= 0 || a.positions);
-  if (turn && tid < a.rot / 2) {
-    // the angle less its whole turns, 2 pi in two doubles
-    const double t = (double)pos * (double)a.inv_freq[tid];
-    const double turns = rint(t * 0.15915494309189534);
-    const double r = fma(-turns, 2.4492935982947064e-16, fma(-turns, 6.283185307179586, t));
-    float s, c;
-    sincosf((float)r, &s, &c);
-    cs[tid] = make_float2(c, a.inverse ? -s : s);
+
+  // the token's position, and its row in the pools
+  int b = 0;
+  long long t = 0, len = 0, pos = -1, row = -1;
+  bool placed = false;
+  if (a.positions) {
+    pos = a.positions[n];
+    placed = true;
+  } else if (find_seq(a, n, &b, &t, &len)) {
+    pos = a.seqlens ? (long long)a.seqlens[b] - len + t : t;
+    placed = pos >= 0;
   }
-  __syncthreads();
-  const float2* f = turn ? cs : nullptr;
-  const int uk = a.Dk / 16;
-  if (a.q_out)
-    for (int i = tid; i < a.Hq * uk; i += kTokThreads) {
-      const int h = i / uk, u = i % uk;
-      rotate_unit(a, f, u, a.q + n * a.qs + h * a.Dk, a.q_out + (n * a.Hq + h) * a.Dk, nullptr);
+  if (a.seqlens && placed) {
+    int page = -1;
+    unsigned slot = 0;
+    if (pos <= INT32_MAX) {                     // not so only for lengths in cu that are none
+      const unsigned col = (unsigned)pos / (unsigned)a.page_size;
+      slot = (unsigned)pos - col * a.page_size;
+      if (col < (unsigned)a.max_pages) page = a.table[(long long)b * a.max_pages + col];
     }
-  if (a.k && (a.k_out || row >= 0))
-    for (int i = tid; i < a.Hkv * uk; i += kTokThreads) {
-      const int h = i / uk, u = i % uk;
-      rotate_unit(a, f, u, a.k + n * a.ks + h * a.Dk,
-                  a.k_out ? a.k_out + (n * a.Hkv + h) * a.Dk : nullptr,
-                  row >= 0 ? a.k_pages + (row * a.Hkv + h) * a.Dk : nullptr);
-    }
-  if (row < 0) return;
-  const int nv = a.Hkv * a.Dv;
-  for (int i = tid * 8; i < nv; i += kTokThreads * 8)
-    *reinterpret_cast<uint4*>(a.v_pages + row * nv + i) =
-        *reinterpret_cast<const uint4*>(a.v + n * a.vs + i);
-  if (a.scalar) {
-    for (int i = tid; i < a.Hkv; i += kTokThreads) a.g_pages[row * a.Hkv + i] = a.g[n * a.gs + i];
-  } else {
-    for (int i = tid * 4; i < nv; i += kTokThreads * 4)
-      *reinterpret_cast<float4*>(a.g_pages + row * nv + i) =
-          *reinterpret_cast<const float4*>(a.g + n * a.gs + i);
+    if ((unsigned)page < (unsigned)a.num_pages) row = (long long)page * a.page_size + slot;
+    else if (a.status && lane == 0) *a.status = FIX_ERR_PAGE;
   }
+
+  const bool turn = a.rot && placed;
+  float4 f[4];
+  if (turn && blockIdx.y * a.items * 32 < qk) {
+    float c[2], s[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int pair = 2 * lane + i;
+      // the angle less its whole turns, 2 pi in two doubles
+      const double w = pair < a.rot / 2 ? (double)pos * (double)a.inv_freq[pair] : 0.0;
+      const double turns = rint(w * 0.15915494309189534);
+      const double r = fma(-turns, 2.4492935982947064e-16, fma(-turns, 6.283185307179586, w));
+      sincospif((float)(r * 0.31830988618379067), &s[i], &c[i]);
+      if (a.inverse) s[i] = -s[i];
+    }
+    cs[warp][lane & 3][lane >> 2] = make_float4(c[0], s[0], c[1], s[1]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = cs[warp][i][u];
+  }
+
+  void *qo = a.q_out + (long long)n * a.Hq * a.Dk, *ko = a.k_out + (long long)n * a.Hkv * a.Dk;
+  void *kp = a.k_pages + row * a.Hkv * a.Dk, *vp = a.v_pages + row * a.Hkv * a.Dv,
+       *gp = a.g_pages + row * a.Hkv * a.Dv;
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int id = first + i * 32;
+    if (i >= a.items || id >= all) break;
+    if (id < qk && turn && turning)
+      rotate_pairs(x[i], y[i], reinterpret_cast<const float2*>(f), a.interleaved);
+    const long long to1 = id < qk ? step : 16;
+    if (id < a.nq || row >= 0) {
+      char* d = const_cast<char*>(unit_of(qo, kp, vp, gp, id));
+      *reinterpret_cast<uint4*>(d) = x[i];
+      *reinterpret_cast<uint4*>(d + to1) = y[i];
+    }
+    if (a.k_out && id >= a.nq && id < qk) {
+      char* d = const_cast<char*>(unit_of(qo, ko, vp, gp, id));
+      *reinterpret_cast<uint4*>(d) = x[i];
+      *reinterpret_cast<uint4*>(d + to1) = y[i];
+    }
+  }
+  if (a.scalar && row >= 0 && blockIdx.y == 0)    // one float per kv head
+    for (int h = lane; h < a.Hkv; h += 32) a.g_pages[row * a.Hkv + h] = a.g[n * a.gs + h];
 }
 
 static bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -225,9 +252,25 @@ fix_status validate_cache(const fix_attn_page_cache* c, const Dims& d) {
   return FIX_OK;
 }
 
-static fix_status launch_tokens(const TokenArgs& a, cudaStream_t st) {
+// Units per lane: eight keep enough loads in flight with few warps; fewer
+// where the tokens are too few to fill the SMs (eight warps on each of the
+// B200's 148) otherwise.
+static fix_status launch_tokens(TokenArgs& a, cudaStream_t st) {
   FIX_ROT_TRY(check_device());
-  token_kernel<<<(unsigned)a.N, kTokThreads, 0, st>>>(a);
+  const long long units = (long long)a.nq + a.nk + a.nv + a.ng;
+  const long long per_lane = units > 32 ? (units + 31) / 32 : 1;
+  int most = 8;
+  while (most > 1 && (long long)a.N * ((per_lane + most - 1) / most) < 148 * 8) most /= 2;
+  long long runs = (per_lane + most - 1) / most;
+  if (runs > 65535) return FIX_ERR_SHAPE;
+  a.items = (int)((per_lane + runs - 1) / runs);
+  const dim3 grid((unsigned)((a.N + kTokWarps - 1) / kTokWarps), (unsigned)runs);
+  switch (most) {
+    case 1: token_kernel<1><<<grid, kTokWarps * 32, 0, st>>>(a); break;
+    case 2: token_kernel<2><<<grid, kTokWarps * 32, 0, st>>>(a); break;
+    case 4: token_kernel<4><<<grid, kTokWarps * 32, 0, st>>>(a); break;
+    default: token_kernel<8><<<grid, kTokWarps * 32, 0, st>>>(a);
+  }
   return launch_status();
 }
 
@@ -259,6 +302,8 @@ extern "C" fix_status fix_attn_rotary(const fix_attn_problem* p, const fix_attn_
   a.k = static_cast<const __nv_bfloat16*>(k);
   a.q_out = static_cast<__nv_bfloat16*>(q_out);
   a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.nq = d.Hq * (d.Dk / 16);
+  a.nk = k ? d.Hkv * (d.Dk / 16) : 0;
   return launch_tokens(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -302,5 +347,9 @@ extern "C" fix_status fix_attn_append_paged(const fix_attn_problem* p, const fix
   a.v_pages = static_cast<__nv_bfloat16*>(c->v_pages);
   a.g_pages = c->g_pages;
   a.status = c->status;
+  a.nq = q ? d.Hq * (d.Dk / 16) : 0;
+  a.nk = d.Hkv * (d.Dk / 16);
+  a.nv = d.Hkv * (d.Dv / 16);
+  a.ng = d.scalar_gate ? 0 : d.Hkv * (d.Dv / 8);
   return launch_tokens(a, static_cast<cudaStream_t>(stream));
 }

@@ -315,6 +315,7 @@ def fix_attn_decode(q, k_cache, v_cache, g_cache, seqlens, o_norm_weight=None, s
 # device index by identity and number, not torch.device objects).
 _Tensor = torch.Tensor
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _need(ok, what):
@@ -371,56 +372,17 @@ def _cuda_index(name, t):
     return index
 
 
-class _On:
-    """Makes device ``index`` current, and ``stream`` where one is given, so
-    that what is allocated meanwhile belongs to the stream that uses it;
-    yields the stream's handle."""
-
-    def __init__(self, index, stream):
-        self.index = index
-        if stream is None:
-            self.ctx = torch.cuda.device(index)
-        else:
-            _need(stream.device.index == index,
-                  f"the stream is on {stream.device}, the tensors on cuda:{index}")
-            self.ctx = torch.cuda.stream(stream)           # sets the device too
-
-    def __enter__(self):
-        self.ctx.__enter__()
-        return _raw_stream(self.index)
-
-    def __exit__(self, *exc):
-        self.ctx.__exit__(*exc)
-
-
-class _Here:
-    """The device and its current stream, both as they are already."""
-
-    def __init__(self, index):
-        self.index = index
-
-    def __enter__(self):
-        return _raw_stream(self.index)
-
-    def __exit__(self, *exc):
-        pass
-
-
-_here = {}
-
-
-def _on(index, stream):
-    if stream is None and torch._C._cuda_getDevice() == index:
-        return _here.get(index) or _here.setdefault(index, _Here(index))
-    return _On(index, stream)
-
-
-def _empty(shape, dtype, index):
-    return torch.empty(shape, dtype=dtype, device=_devices.get(index) or
-                       _devices.setdefault(index, torch.device("cuda", index)))
-
-
-_devices = {}
+def _elsewhere(index, stream):
+    """A context that makes device ``index`` current, and ``stream`` where one
+    is given (so that what is allocated meanwhile belongs to the stream that
+    uses it); None where the call is at home already."""
+    if stream is not None:
+        _need(stream.device.index == index,
+              f"the stream is on {stream.device}, the tensors on cuda:{index}")
+        return torch.cuda.stream(stream)                   # sets the device too
+    if _current_device() != index:
+        return torch.cuda.device(index)
+    return None
 
 
 def _rotation(inv_freq, Dk, interleaved, index):
@@ -457,6 +419,10 @@ def fix_attn_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved
     output.  ``inverse`` turns back (the gradient).  Returns new dense (q, k),
     or ``out`` = (q_out, k_out), which may be dense inputs themselves."""
     index = _cuda_index("q", q)
+    ctx = _elsewhere(index, stream)
+    if ctx is not None:
+        with ctx:
+            return fix_attn_rotary(q, k, inv_freq, cu_seqlens, positions, interleaved, inverse, out)
     _tensor("q", q, torch.bfloat16, index)
     _need(q.dim() == 4, "q must be [B,T,Hq,Dk]")
     B, T, Hq, Dk = q.shape
@@ -473,19 +439,19 @@ def fix_attn_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved
     if positions is not None:
         _dense("positions", positions, torch.int32, index, (B, T))
     qs = _token_stride("q", q, Hq * Dk)
-    with _on(index, stream) as st:
-        if out is None:
-            q_out = _empty((B, T, Hq, Dk), torch.bfloat16, index)
-            k_out = _empty((B, T, Hkv, Dk), torch.bfloat16, index) if k is not None else None
-        else:
-            q_out, k_out = out
-            _dense("out[0]", q_out, torch.bfloat16, index, (B, T, Hq, Dk))
-            _need((k is None) == (k_out is None), "out[1] goes with k")
-            if k is not None:
-                _dense("out[1]", k_out, torch.bfloat16, index, (B, T, Hkv, Dk))
-        s = load().fix_attn_rotary(
-            p, r, None if positions is None else positions.data_ptr(), q.data_ptr(), qs, kp, ks,
-            q_out.data_ptr(), None if k is None else k_out.data_ptr(), 1 if inverse else 0, st)
+    if out is None:
+        q_out = q.new_empty((B, T, Hq, Dk))
+        k_out = k.new_empty((B, T, Hkv, Dk)) if k is not None else None
+    else:
+        q_out, k_out = out
+        _dense("out[0]", q_out, torch.bfloat16, index, (B, T, Hq, Dk))
+        _need((k is None) == (k_out is None), "out[1] goes with k")
+        if k is not None:
+            _dense("out[1]", k_out, torch.bfloat16, index, (B, T, Hkv, Dk))
+    s = load().fix_attn_rotary(
+        p, r, None if positions is None else positions.data_ptr(), q.data_ptr(), qs, kp, ks,
+        q_out.data_ptr(), None if k is None else k_out.data_ptr(), 1 if inverse else 0,
+        _raw_stream(index))
     if s != 0:
         raise FixStatusError(s, "fix_attn_rotary")
     return q_out, k_out
@@ -535,6 +501,11 @@ def fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlen
     rotated: None without ``q`` / unless ``return_k``.  ``status`` (int32 [1])
     is set to FIX_ERR_PAGE if a token had no page (it is skipped)."""
     index = _cuda_index("k", k)
+    ctx = _elsewhere(index, stream)
+    if ctx is not None:
+        with ctx:
+            return fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlens,
+                                         cu_seqlens, q, inv_freq, interleaved, return_k, status)
     _tensor("k", k, torch.bfloat16, index)
     _tensor("v", v, torch.bfloat16, index)
     _tensor("g", g, torch.float32, index)
@@ -564,13 +535,12 @@ def fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlen
     ks = _token_stride("k", k, Hkv * Dk)
     vs = _token_stride("v", v, Hkv * Dv)
     gs = _token_stride("g", g, Hkv if scalar else Hkv * Dv)
-    with _on(index, stream) as st:
-        q_out = _empty((B, T, Hq, Dk), torch.bfloat16, index) if q is not None else None
-        k_out = _empty((B, T, Hkv, Dk), torch.bfloat16, index) if return_k else None
-        s = load().fix_attn_append_paged(
-            p, c, r, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), gs,
-            None if q_out is None else q_out.data_ptr(),
-            None if k_out is None else k_out.data_ptr(), st)
+    q_out = q.new_empty((B, T, Hq, Dk)) if q is not None else None
+    k_out = k.new_empty((B, T, Hkv, Dk)) if return_k else None
+    s = load().fix_attn_append_paged(
+        p, c, r, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), gs,
+        None if q_out is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
+        _raw_stream(index))
     if s != 0:
         raise FixStatusError(s, "fix_attn_append_paged")
     return q_out, k_out
@@ -598,8 +568,8 @@ def fix_attn_decode_paged_workspace(q, k_pages, v_pages, g_pages, page_table, se
     not overlap (uint8 tensor; needs no initialisation)."""
     index, p, c, _ = _paged_problem(q, k_pages, v_pages, g_pages, page_table, seqlens, None, 1e-6,
                                     torch.bfloat16, True, None)
-    return _empty(max(int(load().fix_attn_decode_paged_workspace_bytes(p, c)), 1), torch.uint8,
-                  index)
+    return torch.empty(max(load().fix_attn_decode_paged_workspace_bytes(p, c), 1),
+                       dtype=torch.uint8, device=q.device)
 
 
 def fix_attn_decode_paged(q, k_pages, v_pages, g_pages, page_table, seqlens, o_norm_weight=None,
@@ -611,6 +581,12 @@ def fix_attn_decode_paged(q, k_pages, v_pages, g_pages, page_table, seqlens, o_n
     contiguous cache.  int32 ``seqlens`` [B] on the device; length 0 gives 0.
     ``status`` (int32 [1]) is set to FIX_ERR_PAGE if a token had no page (it
     is left out).  Returns y [B,Hq,Dv]."""
+    ctx = _elsewhere(_cuda_index("q", q), stream)
+    if ctx is not None:
+        with ctx:
+            return fix_attn_decode_paged(q, k_pages, v_pages, g_pages, page_table, seqlens,
+                                         o_norm_weight, scale, eps, y_dtype, o_gate, o_norm,
+                                         workspace, out, status)
     index, p, c, shape = _paged_problem(q, k_pages, v_pages, g_pages, page_table, seqlens, scale,
                                         eps, y_dtype, o_norm, status)
     _need(o_norm_weight is not None or not o_norm, "o_norm=True needs o_norm_weight")
@@ -622,19 +598,20 @@ def fix_attn_decode_paged(q, k_pages, v_pages, g_pages, page_table, seqlens, o_n
         _dense("o_gate", o_gate, torch.bfloat16, index, shape)
         zp = o_gate.data_ptr()
     lib = load()
-    with _on(index, stream) as st:
-        if out is None:
-            out = _empty(shape, y_dtype, index)
-        else:
-            _dense("out", out, y_dtype, index, shape)
-        if workspace is None:
-            workspace = _empty(max(lib.fix_attn_decode_paged_workspace_bytes(p, c), 1),
-                               torch.uint8, index)
-        else:
-            _tensor("workspace", workspace, torch.uint8, index)
-            _need(workspace.is_contiguous(), "workspace must be contiguous")
-        s = lib.fix_attn_decode_paged(p, c, q.data_ptr(), wp, zp, out.data_ptr(),
-                                      workspace.data_ptr(), workspace.numel(), st)
+    if out is None:
+        out = q.new_empty(shape) if y_dtype is torch.bfloat16 else q.new_empty(shape, dtype=y_dtype)
+    else:
+        _dense("out", out, y_dtype, index, shape)
+    if workspace is None:
+        # in q's type: a plain new_empty is the cheapest allocation
+        nbytes = lib.fix_attn_decode_paged_workspace_bytes(p, c)
+        workspace = q.new_empty((nbytes + 1) // 2)
+    else:
+        _tensor("workspace", workspace, torch.uint8, index)
+        _need(workspace.is_contiguous(), "workspace must be contiguous")
+        nbytes = workspace.numel()
+    s = lib.fix_attn_decode_paged(p, c, q.data_ptr(), wp, zp, out.data_ptr(), workspace.data_ptr(),
+                                  nbytes, _raw_stream(index))
     if s != 0:
         raise FixStatusError(s, "fix_attn_decode_paged")
     return out
