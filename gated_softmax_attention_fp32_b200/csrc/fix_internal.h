@@ -7,8 +7,38 @@ namespace fix {
 
 constexpr int ST_ROWS = 32;  // rows per CTA of the exact (SIMT) kernels
 
+// FIX_OK if no launch error is pending, else FIX_ERR_CUDA (test builds
+// record the error for fix_attn_test_last_cuda_error).
+fix_status launch_status();
 // Validates a problem descriptor and fills the kernel-side dims (fix_api.cu).
 fix_status validate_problem(const fix_attn_problem* p, Dims* d);
+// A launch whose CTAs may be put in place when those of the kernel before it on
+// the stream have left, before that kernel's end is signalled (programmatic
+// dependent launch; 1 to 2 us less between two kernels): the kernel waits
+// (griddepcontrol.wait) before it touches memory.  Kernels do not let the next
+// one in any earlier (griddepcontrol.launch_dependents): it would share SMs
+// with their last CTAs and keep to an uneven placement for its whole run
+// (decode of 64 unequal sequences: 133 us instead of 106).
+struct OverlappedLaunch {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  OverlappedLaunch(dim3 grid, int threads, size_t smem, cudaStream_t st) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+  }
+  OverlappedLaunch(const OverlappedLaunch&) = delete;
+  template <typename Args>
+  fix_status run(void (*kernel)(Args), const Args& a) const {
+    cudaLaunchKernelEx(&cfg, kernel, a);
+    return launch_status();
+  }
+};
 // FIX_OK if the current device is sm_100 (fix_api.cu).
 fix_status check_device();
 // Validates the sizes and pointers of a paged cache for `d` (fix_rotary.cu).
@@ -74,9 +104,6 @@ __global__ void dkv_simt_kernel(Dims d, const Chunk* chunks, const __nv_bfloat16
 // increase, so the launch path makes no further runtime calls for it (which
 // keeps the calls cheap and lets a stream capture record the launches).
 bool set_smem_limit(const void* func, int bytes);
-// FIX_OK if no launch error is pending, else FIX_ERR_CUDA (test builds
-// record the error for fix_attn_test_last_cuda_error).
-fix_status launch_status();
 bool tc_fwd_supported(const Dims& d);
 fix_status tc_fwd(const Dims& d, const Chunk* chunks, const int* order, const void* q,
                   const void* k, const uint16_t* vt, const __nv_bfloat16* vm,

@@ -45,13 +45,17 @@ constexpr int kTileKeys = 16;
 constexpr int kPagedWarps = 4;         // warps per CTA of the split kernel
 constexpr int kJoinWarps = 16;         // at most, per CTA
 constexpr int kSMs = 148;              // B200
-constexpr int kUnitCost = 2;           // line positions of a unit beside its tiles
+// Line positions of a unit beside its tiles.  0 leaves whole spans of one-tile
+// units to single warps (64 unequal sequences: 161 us instead of 105); 1 to 4
+// differ by 2 to 4%.
+constexpr int kUnitCost = 3;
 
 struct PagedArgs {
   int B, Hq, Hkv, Dk, grp, no_norm, y_f32;
   int nhb, hpb;                        // head blocks per group, heads per block
   float scale_log2, eps;
   int page_size, num_pages, max_pages;
+  int page_shift;                      // log2 of the page size, or -1
   const int *table, *seqlens;
   const __nv_bfloat16 *q, *k, *v, *w, *z;
   const float* g;
@@ -61,7 +65,6 @@ struct PagedArgs {
   long long slot_floats;               // floats per slot: hpb (DV + 2) + DV
   float* slots;                        // two per worker
   int4* jobs;                          // the join's work: (pieces, first worker, unit)
-  int units;                           // B * Hkv * nhb
   int join_by_unit, heads_per_cta, warps_per_head;   // shape of the join
 };
 
@@ -70,45 +73,45 @@ __device__ __forceinline__ int paged_len(const PagedArgs& a, int b) {
   const int L = a.seqlens[b];
   return L <= 0 ? 0 : (L > cap ? (int)cap : L);
 }
+__device__ __forceinline__ int tiles_of(int len) {
+  return (int)(((unsigned)len + kTileKeys - 1) / kTileKeys);
+}
 __device__ __forceinline__ int paged_tiles(const PagedArgs& a, int b) {
-  return (int)(((unsigned)paged_len(a, b) + kTileKeys - 1) / kTileKeys);
+  return tiles_of(paged_len(a, b));
 }
-// Line positions of one unit of sequence b.
-__device__ __forceinline__ int paged_cost(const PagedArgs& a, int b) {
-  const int n = paged_tiles(a, b);
-  return n ? n + kUnitCost : 0;
-}
+// Line positions of one unit of n tiles.
+__device__ __forceinline__ int paged_cost(int n) { return n ? n + kUnitCost : 0; }
 
 // The line over all sequences, for a whole warp: lane i sums a run of K
-// sequences, their positions per unit.
+// sequences.  (The host refuses sizes whose line could pass 2^31 positions.)
 struct Line {
   int K;
-  long long mine, upto;        // of this lane's run; of the runs up to it
-  __device__ __forceinline__ explicit Line(const PagedArgs& a) {
+  int mine, upto;        // positions of this lane's run; of the runs up to it
+  __device__ __forceinline__ Line(const PagedArgs& a, int upb) {
     const int lane = threadIdx.x & 31;
     K = (a.B + 31) / 32;
     mine = 0;
 #pragma unroll 8
-    for (int i = lane * K; i < min(a.B, (lane + 1) * K); ++i) mine += paged_cost(a, i);
+    for (int i = lane * K; i < min(a.B, (lane + 1) * K); ++i) mine += paged_cost(paged_tiles(a, i));
+    mine *= upb;
     upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += x;
     }
   }
-  __device__ __forceinline__ long long total() const {
-    return __shfl_sync(0xffffffffu, upto, 31);
-  }
-  // The sequence that holds position pos < total() * upb of the line of upb
-  // units per sequence, and where it starts.
-  __device__ __forceinline__ void find(const PagedArgs& a, long long pos, int upb, int* b,
-                                       long long* start) const {
-    const int src = __ffs(__ballot_sync(0xffffffffu, upto * upb > pos)) - 1;
-    long long at = __shfl_sync(0xffffffffu, (upto - mine) * upb, src);
+  __device__ __forceinline__ int total() const { return __shfl_sync(0xffffffffu, upto, 31); }
+  // The sequence that holds position pos < total(), its length and where it
+  // starts.
+  __device__ __forceinline__ void find(const PagedArgs& a, int pos, int upb, int* b, int* len,
+                                       int* start) const {
+    const int src = __ffs(__ballot_sync(0xffffffffu, upto > pos)) - 1;
+    int at = __shfl_sync(0xffffffffu, upto - mine, src);
     int i = src * K;
     for (;;) {
-      const long long t = (long long)paged_cost(a, i) * upb;
+      *len = paged_len(a, i);
+      const int t = paged_cost(tiles_of(*len)) * upb;
       if (pos < at + t || i + 1 >= a.B) break;
       at += t;
       ++i;
@@ -266,33 +269,17 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
   char* sq = mine + ST * stage_bytes;
   const int upb = a.Hkv * a.nhb;
 
-  // sequences without a token
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const int L = a.seqlens[b];
-    if (L > 0) {
-      if (a.status && threadIdx.x == 0 && L > (long long)a.max_pages * a.page_size)
-        *a.status = FIX_ERR_PAGE;
-      continue;
-    }
-    for (int e = threadIdx.x; e < a.Hq * DV; e += blockDim.x) {
-      const size_t at = (size_t)b * a.Hq * DV + e;
-      if (a.y_f32) reinterpret_cast<float*>(a.y)[at] = 0.f;
-      else reinterpret_cast<__nv_bfloat16*>(a.y)[at] = f2bf(0.f);
-    }
-    if (a.join_by_unit)
-      for (int u = threadIdx.x; u < upb; u += blockDim.x)
-        a.jobs[b * upb + u] = make_int4(0, 0, 0, 0);
-  }
-
-  const Line line(a);
-  const long long total = line.total() * upb;
+  // this kernel's inputs are there when the one before it has ended
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Line line(a, upb);
+  const int total = line.total();
   const int worker = warp * gridDim.x + blockIdx.x;
-  const long long span = (total + a.nworkers - 1) / a.nworkers;
-  const long long first = span * worker, last = min(total, first + span);
+  const int span = (int)(((unsigned)total + a.nworkers - 1) / a.nworkers);
+  const int first = (int)min((long long)span * worker, (long long)total);
+  const int last = first + min(span, total - first);
   int4 job = make_int4(0, 0, 0, 0);      // the unit that begins here and ends beyond
-  int b = 0;
-  long long base = 0;                    // line position of sequence b
-  if (first < last) line.find(a, first, upb, &b, &base);
+  int b = 0, L = 0, base = 0;            // sequence, its length and line position
+  if (first < last) line.find(a, first, upb, &b, &L, &base);
 
   // lane roles
   const int j = lane & 3, r8 = lane & 7;
@@ -304,58 +291,63 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
   const int kshift = 31 - __clz(Dk / 8);
   const bool whole_pages = a.page_size % kTileKeys == 0;    // a tile lies in one page
 
-  for (long long pos = first; pos < last;) {
-    const int L = paged_len(a, b);
-    const int nb = (int)(((unsigned)L + kTileKeys - 1) / kTileKeys);
-    const int cost = nb ? nb + kUnitCost : 0;
-    if (pos >= base + (long long)cost * upb) {              // next sequence
-      base += (long long)cost * upb;
-      ++b;
+  for (int pos = first; pos < last;) {
+    const int nb = tiles_of(L), cost = paged_cost(nb);
+    if (pos - base >= cost * upb) {                         // next sequence
+      base += cost * upb;
+      L = paged_len(a, ++b);
       continue;
     }
-    const int u = (int)((pos - base) / cost);               // unit of the sequence
-    const long long live = base + (long long)u * cost + kUnitCost;   // position of its tile 0
-    const int t0 = (int)max(0LL, pos - live);
-    const int t1 = (int)min((long long)nb, last - live);
-    pos = live + max(t0, t1);
-    if (t1 <= t0) {
-      if (pos > last) break;
-      continue;
-    }
-    const int kv = u / a.nhb, hb = u - kv * a.nhb;
+    const int u = (int)((unsigned)(pos - base) / (unsigned)cost);   // unit of the sequence
+    const int live = base + u * cost + kUnitCost;         // position of its tile 0
+    const int t0 = max(0, pos - live), t1 = min(nb, last - live);
+    if (t1 <= t0) break;                                    // only its start lies in this span
+    pos = live + t1;
+    const int kv = a.nhb == 1 ? u : u / a.nhb, hb = u - kv * a.nhb;
     const int h0 = kv * a.grp + hb * a.hpb;                 // first q head
     const int nh = min(a.hpb, a.grp - hb * a.hpb);          // q heads
     const int n = t1 - t0;
     const int* table = a.table + (long long)b * a.max_pages;
 
-    // row of key (lane & 15) of a tile in the pools, and which keys are there
-    auto lookup = [&](int tile, uint32_t& row, uint32_t& mask) {
-      const unsigned s = (unsigned)tile * kTileKeys + (lane & 15);
-      int page = -1;
-      unsigned slot = 0;
-      if (s < (unsigned)L) {
-        const unsigned col = s / (unsigned)a.page_size;
-        slot = s - col * a.page_size;
-        page = table[col];
-        if ((unsigned)page >= (unsigned)a.num_pages) {
-          page = -1;
-          if (a.status) *a.status = FIX_ERR_PAGE;
-        }
+    // Where the keys of two tiles are: lane i has key i of the pair of tiles
+    // 2 p and 2 p + 1.  fetch() starts the read of the page table, a pair ahead
+    // of its use; rows() ends it: the key's row in the pools, and which keys
+    // are there.
+    auto fetch = [&](int pair) {
+      const unsigned s = (unsigned)pair * 32 + lane;
+      if (pair < 0 || s >= (unsigned)L) return -1;
+      return table[a.page_shift >= 0 ? s >> a.page_shift : s / (unsigned)a.page_size];
+    };
+    uint32_t row = 0, mask = 0;
+    auto rows = [&](int pair, int page) {
+      const unsigned s = (unsigned)pair * 32 + lane;
+      const unsigned slot =
+          a.page_shift >= 0 ? s & (a.page_size - 1) : s % (unsigned)a.page_size;
+      const bool there = (unsigned)page < (unsigned)a.num_pages;
+      if (!there && s < (unsigned)L && a.status) *a.status = FIX_ERR_PAGE;
+      row = there ? ((uint32_t)page * a.page_size + slot) * a.Hkv + kv : 0u;
+      mask = __ballot_sync(0xffffffffu, there);
+    };
+    int page = -1;                         // of the pair below the current one
+    auto step = [&](int tile) {            // before a tile is copied; tiles go down
+      if (tile & 1) {
+        rows(tile >> 1, page);
+        page = fetch((tile >> 1) - 1);
       }
-      row = page < 0 ? 0u : ((uint32_t)page * a.page_size + slot) * a.Hkv + kv;
-      mask = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
     };
     // Tiles go to shared memory in rows of keys, 16-byte chunk c of key s at
     // chunk c ^ (s % 8): matrix loads and the gates' reads meet no conflicts.
     // A full tile of one page has evenly spaced rows; keys that are not there
     // are filled with zeros.
-    auto copy_k = [&](int stage, uint32_t row, uint32_t mask) {
+    auto copy_k = [&](int stage, int tile) {
+      const int from = (tile & 1) * 16;    // lane of the tile's first key
+      const uint32_t there = mask >> from & 0xffffu;
       const uint32_t dst = ring + stage * stage_bytes;
       const int c = lane & ((1 << kshift) - 1), per = 32 >> kshift;
       int key = lane >> kshift;
-      if (whole_pages && mask == 0xffffu) {
+      if (whole_pages && there == 0xffffu) {
         const __nv_bfloat16* src =
-            a.k + (size_t)(__shfl_sync(0xffffffffu, row, 0) + key * a.Hkv) * Dk + c * 8;
+            a.k + (size_t)(__shfl_sync(0xffffffffu, row, from) + key * a.Hkv) * Dk + c * 8;
         const size_t step = (size_t)per * a.Hkv * Dk;
 #pragma unroll 8
         for (int it = 0; it < Dk / 16; ++it, key += per, src += step)
@@ -363,19 +355,21 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
       } else {
 #pragma unroll 1
         for (int it = 0; it < Dk / 16; ++it, key += per) {
-          const uint32_t rr = __shfl_sync(0xffffffffu, row, key);
+          const uint32_t rr = __shfl_sync(0xffffffffu, row, from + key);
           copy16(dst + key * kpitch + ((c ^ (key & 7)) << 4), a.k + (size_t)rr * Dk + c * 8,
-                 (mask >> key) & 1);
+                 (there >> key) & 1);
         }
       }
     };
-    auto copy_vg = [&](int stage, uint32_t row, uint32_t mask) {
+    auto copy_vg = [&](int stage, int tile) {
+      const int from = (tile & 1) * 16;
+      const uint32_t there = mask >> from & 0xffffu;
       const uint32_t dst = ring + stage * stage_bytes + kTileKeys * kpitch;
       const uint32_t gdst = dst + R::kV;
       constexpr int CV = DV / 8, CG = DV / 4;               // chunks per row
       const int vc = lane % CV, gc = lane % CG;
-      if (whole_pages && mask == 0xffffu) {
-        const uint32_t row0 = __shfl_sync(0xffffffffu, row, 0);
+      if (whole_pages && there == 0xffffu) {
+        const uint32_t row0 = __shfl_sync(0xffffffffu, row, from);
         const __nv_bfloat16* src = a.v + (size_t)(row0 + (lane / CV) * a.Hkv) * DV + vc * 8;
         const size_t vstep = (size_t)(32 / CV) * a.Hkv * DV;
 #pragma unroll
@@ -396,40 +390,45 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll 1
         for (int it = 0; it < DV / 16; ++it) {
           const int key = it * (32 / CV) + lane / CV;
-          const uint32_t rr = __shfl_sync(0xffffffffu, row, key);
+          const uint32_t rr = __shfl_sync(0xffffffffu, row, from + key);
           copy16(dst + key * R::kVPitch + ((vc ^ (key & 7)) << 4), a.v + (size_t)rr * DV + vc * 8,
-                 (mask >> key) & 1);
+                 (there >> key) & 1);
         }
         if constexpr (!SCALAR) {
 #pragma unroll 1
           for (int it = 0; it < DV / 8; ++it) {
             const int key = it * (32 / CG) + lane / CG;
-            const uint32_t rr = __shfl_sync(0xffffffffu, row, key);
+            const uint32_t rr = __shfl_sync(0xffffffffu, row, from + key);
             copy16(gdst + key * R::kGPitch + ((gc ^ (key & 7)) << 4), a.g + (size_t)rr * DV + gc * 4,
-                   (mask >> key) & 1);
+                   (there >> key) & 1);
           }
         }
       }
       if constexpr (SCALAR)
-        if (lane < kTileKeys) copy4(gdst + lane * 4, a.g + row, (mask >> lane) & 1);
+        if ((lane & 16) == from) copy4(gdst + (lane & 15) * 4, a.g + row, mask >> lane & 1);
     };
 
-    uint32_t row, mask, masks[ST];
-    lookup(t1 - 1, row, mask);
+    uint32_t masks[ST];
+    const int page0 = fetch((t1 - 1) >> 1);
+    page = fetch(((t1 - 1) >> 1) - 1);
     // the block's queries, rows of 8 NT heads (zero beyond nh)
     for (int i = lane; i < NT * 8 << kshift; i += 32) {
       const int h = i >> kshift, c = i & ((1 << kshift) - 1);
       copy16(smem_addr(sq + h * qpitch + c * 16),
              a.q + ((size_t)b * a.Hq + h0 + min(h, nh - 1)) * Dk + c * 8, h < nh);
     }
+    rows((t1 - 1) >> 1, page0);
+    int tile = t1 - 1;                     // the next one to copy
 #pragma unroll
     for (int s = 0; s < ST; ++s) {
-      masks[s] = mask;
-      if (s < n) copy_k(s, row, mask);
+      if (s < n) {
+        if (s) step(tile);
+        masks[s] = mask >> (tile & 1) * 16 & 0xffffu;
+        copy_k(s, tile);
+      }
       cp_async_commit();
-      if (s < n) copy_vg(s, row, mask);
+      if (s < n) copy_vg(s, tile--);
       cp_async_commit();
-      if (s + 1 < n) lookup(t1 - 2 - s, row, mask);
     }
 
     float acc[MT][NT][4];
@@ -474,7 +473,11 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
         }
       }
       __syncwarp();
-      if (i + ST < n) copy_k(stage, row, mask);
+      const bool more = i + ST < n;
+      if (more) {
+        step(tile);
+        copy_k(stage, tile);
+      }
       cp_async_commit();
 
       // softmax of the tile against the running maximum
@@ -622,11 +625,12 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
         }
       }
       __syncwarp();
-      if (i + ST < n) copy_vg(stage, row, mask);
-      cp_async_commit();
       if constexpr (ST == 2) masks[0] = masks[1];
-      masks[ST - 1] = mask;
-      if (i + ST + 1 < n) lookup(t1 - 2 - ST - i, row, mask);
+      if (more) {
+        masks[ST - 1] = mask >> (tile & 1) * 16 & 0xffffu;
+        copy_vg(stage, tile--);
+      }
+      cp_async_commit();
     }
 
     // The piece's rows go through the ring (its tiles are used up), so that
@@ -686,7 +690,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
       if (in_row) store_n<VPL>(tail + c0, suf);
       if (lane < 2 * nh) tail[DV + lane] = sml[lane];
       if (t0 == 0) {
-        const int wl = (int)((live + nb - 1) / span);
+        const int wl = (live + nb - 1) / span;
         job = make_int4(wl - worker + 1, worker, b * upb + u, 0);
         if (a.join_by_unit && lane == 0) a.jobs[b * upb + u] = job;
       }
@@ -694,6 +698,24 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
     __syncwarp();
   }
   if (!a.join_by_unit && lane == 0) a.jobs[worker] = job;
+
+  // sequences without a token
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const int L = a.seqlens[b];
+    if (L > 0) {
+      if (a.status && threadIdx.x == 0 && L > (long long)a.max_pages * a.page_size)
+        *a.status = FIX_ERR_PAGE;
+      continue;
+    }
+    for (int e = threadIdx.x; e < a.Hq * DV; e += blockDim.x) {
+      const size_t at = (size_t)b * a.Hq * DV + e;
+      if (a.y_f32) reinterpret_cast<float*>(a.y)[at] = 0.f;
+      else reinterpret_cast<__nv_bfloat16*>(a.y)[at] = f2bf(0.f);
+    }
+    if (a.join_by_unit)
+      for (int u = threadIdx.x; u < upb; u += blockDim.x)
+        a.jobs[b * upb + u] = make_int4(0, 0, 0, 0);
+  }
 }
 
 // Joins the pieces of the units that were cut.  grid.x: the units, or (where
@@ -701,8 +723,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 // begins in its span; grid.y: the head blocks' heads, heads_per_cta at a time.
 // A head has warps_per_head warps, each for a run of its pieces, newest first
 // and four loads deep (what it costs is the latency of its loads); channels
-// lie over the lanes.  Launched so that its CTAs are in place when
-// the split kernel ends.
+// lie over the lanes.
 template <int DV>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     paged_join_kernel(const __grid_constant__ PagedArgs a) {
@@ -816,8 +837,8 @@ static int paged_smem_bytes(const Dims& d) {
 }
 
 struct PagedPlan {
-  int nt, hpb, nhb, units, ctas, workers, smem, jobs;
-  long long slot_floats;
+  int nt, hpb, nhb, ctas, workers, smem, jobs;
+  long long units, slot_floats;
   size_t job_bytes, bytes;
 };
 
@@ -831,7 +852,7 @@ static PagedPlan paged_plan(const Dims& d, const fix_attn_page_cache* c) {
   p.nt = paged_nt(d);
   p.hpb = d.grp < 8 * p.nt ? d.grp : 8 * p.nt;
   p.nhb = (d.grp + p.hpb - 1) / p.hpb;
-  p.units = d.B * d.Hkv * p.nhb;
+  p.units = (long long)d.B * d.Hkv * p.nhb;
   p.smem = paged_smem_bytes(d);
   const int fit = 228 * 1024 / (p.smem + 1024);
   const int per_sm = fit < (p.nt == 1 ? 3 : 2) ? fit : (p.nt == 1 ? 3 : 2);
@@ -841,7 +862,7 @@ static PagedPlan paged_plan(const Dims& d, const fix_attn_page_cache* c) {
   p.ctas = tiles < (long long)kSMs * per_sm ? (int)tiles : kSMs * per_sm;
   p.workers = p.ctas * kPagedWarps;
   p.slot_floats = ((long long)p.hpb * (d.Dv + 2) + d.Dv + 31) / 32 * 32;
-  p.jobs = p.units < p.workers ? p.units : p.workers;
+  p.jobs = p.units < p.workers ? (int)p.units : p.workers;
   p.job_bytes = ((size_t)p.jobs * sizeof(int4) + 255) / 256 * 256;
   p.bytes = p.job_bytes + (size_t)p.workers * 2 * p.slot_floats * 4;
   return p;
@@ -852,27 +873,23 @@ static fix_status paged_dims(const fix_attn_problem* p, const fix_attn_page_cach
   if (p->cu_seqlens || p->num_seqs) return FIX_ERR_CU_SEQLENS;   // lengths come with the cache
   if (p->seqlen != 1) return FIX_ERR_SHAPE;
   if ((long long)d->B * d->Hq > (1 << 28)) return FIX_ERR_SHAPE;
-  return validate_cache(c, *d);
+  FIX_PAGED_TRY(validate_cache(c, *d));
+  // the line of tiles is counted in 32 bits
+  long long cap = (long long)c->max_pages * c->page_size;
+  if (cap > INT32_MAX) cap = INT32_MAX;
+  const PagedPlan pl = paged_plan(*d, c);
+  const long long line = ((cap + kTileKeys - 1) / kTileKeys + kUnitCost) * pl.units;
+  return line < INT32_MAX ? FIX_OK : FIX_ERR_SHAPE;
 }
 
 template <int DV, int NT, bool SCALAR>
 static fix_status paged_launch(const PagedArgs& a, const PagedPlan& pl, cudaStream_t st) {
   auto* kernel = paged_decode_kernel<DV, NT, SCALAR>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), pl.smem)) return FIX_ERR_CUDA;
-  kernel<<<pl.ctas, kPagedWarps * 32, pl.smem, st>>>(a);
-  FIX_PAGED_TRY(launch_status());
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(pl.jobs,
-                     (a.hpb + a.heads_per_cta - 1) / a.heads_per_cta);
-  cfg.blockDim = dim3(a.heads_per_cta * a.warps_per_head * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, a);
-  return launch_status();
+  FIX_PAGED_TRY(OverlappedLaunch(dim3(pl.ctas), kPagedWarps * 32, pl.smem, st).run(kernel, a));
+  return OverlappedLaunch(dim3(pl.jobs, (a.hpb + a.heads_per_cta - 1) / a.heads_per_cta),
+                          a.heads_per_cta * a.warps_per_head * 32, 0, st)
+      .run(paged_join_kernel<DV>, a);
 }
 
 template <int DV>
@@ -912,6 +929,9 @@ extern "C" fix_status fix_attn_decode_paged(const fix_attn_problem* p, const fix
   a.nhb = pl.nhb; a.hpb = pl.hpb;
   a.scale_log2 = d.scale * kLog2e; a.eps = d.eps;
   a.page_size = c->page_size; a.num_pages = c->num_pages; a.max_pages = c->max_pages;
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (c->page_size == 1 << i) a.page_shift = i;
   a.table = c->page_table; a.seqlens = c->seqlens;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k = static_cast<const __nv_bfloat16*>(c->k_pages);
@@ -925,7 +945,6 @@ extern "C" fix_status fix_attn_decode_paged(const fix_attn_problem* p, const fix
   a.slot_floats = pl.slot_floats;
   a.jobs = static_cast<int4*>(workspace);
   a.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.job_bytes);
-  a.units = pl.units;
   // warps per head: about one per piece that a unit of average length has, up
   // to some 4096 in all (28 per SM); CTAs of four warps at least
   a.join_by_unit = pl.units <= pl.workers;

@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kTokWarps * 32) token_kernel(const __grid_cons
   __shared__ float4 cs[kTokWarps][4][8];        // (cos, sin) of pairs 8 u + 2 i, + 1 at [i][u]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = blockIdx.x * kTokWarps + warp;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (n >= a.N) return;
   const int uk = a.Dk / 16, u = lane & (uk - 1);
   const int first = blockIdx.y * a.items * 32 + lane;
@@ -264,14 +265,14 @@ static fix_status launch_tokens(TokenArgs& a, cudaStream_t st) {
   long long runs = (per_lane + most - 1) / most;
   if (runs > 65535) return FIX_ERR_SHAPE;
   a.items = (int)((per_lane + runs - 1) / runs);
-  const dim3 grid((unsigned)((a.N + kTokWarps - 1) / kTokWarps), (unsigned)runs);
+  const OverlappedLaunch launch(dim3((a.N + kTokWarps - 1) / kTokWarps, (unsigned)runs),
+                                kTokWarps * 32, 0, st);
   switch (most) {
-    case 1: token_kernel<1><<<grid, kTokWarps * 32, 0, st>>>(a); break;
-    case 2: token_kernel<2><<<grid, kTokWarps * 32, 0, st>>>(a); break;
-    case 4: token_kernel<4><<<grid, kTokWarps * 32, 0, st>>>(a); break;
-    default: token_kernel<8><<<grid, kTokWarps * 32, 0, st>>>(a);
+    case 1: return launch.run(token_kernel<1>, a);
+    case 2: return launch.run(token_kernel<2>, a);
+    case 4: return launch.run(token_kernel<4>, a);
+    default: return launch.run(token_kernel<8>, a);
   }
-  return launch_status();
 }
 
 }  // namespace fix

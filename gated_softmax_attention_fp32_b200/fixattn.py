@@ -314,6 +314,7 @@ def fix_attn_decode(q, k_cache, v_cache, g_cache, seqlens, o_norm_weight=None, s
 # few microseconds: they ask a tensor for no more than they need (dtype and
 # device index by identity and number, not torch.device objects).
 _Tensor = torch.Tensor
+_bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -423,12 +424,12 @@ def fix_attn_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved
     if ctx is not None:
         with ctx:
             return fix_attn_rotary(q, k, inv_freq, cu_seqlens, positions, interleaved, inverse, out)
-    _tensor("q", q, torch.bfloat16, index)
+    _tensor("q", q, _bf16, index)
     _need(q.dim() == 4, "q must be [B,T,Hq,Dk]")
     B, T, Hq, Dk = q.shape
     Hkv, ks, kp = Hq, 0, None
     if k is not None:
-        _tensor("k", k, torch.bfloat16, index)
+        _tensor("k", k, _bf16, index)
         _need(k.dim() == 4, "k must be [B,T,Hkv,Dk]")
         Bk, Tk, Hkv, Dkk = k.shape
         _need(Bk == B and Tk == T and Dkk == Dk, "k must have q's B, T and Dk")
@@ -437,17 +438,17 @@ def fix_attn_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved
     r = _rotation(inv_freq, Dk, interleaved, index)
     p = _token_problem(Hq, Hkv, B, T, Dk, Dk, cu_seqlens, index)
     if positions is not None:
-        _dense("positions", positions, torch.int32, index, (B, T))
+        _dense("positions", positions, _i32, index, (B, T))
     qs = _token_stride("q", q, Hq * Dk)
     if out is None:
         q_out = q.new_empty((B, T, Hq, Dk))
         k_out = k.new_empty((B, T, Hkv, Dk)) if k is not None else None
     else:
         q_out, k_out = out
-        _dense("out[0]", q_out, torch.bfloat16, index, (B, T, Hq, Dk))
+        _dense("out[0]", q_out, _bf16, index, (B, T, Hq, Dk))
         _need((k is None) == (k_out is None), "out[1] goes with k")
         if k is not None:
-            _dense("out[1]", k_out, torch.bfloat16, index, (B, T, Hkv, Dk))
+            _dense("out[1]", k_out, _bf16, index, (B, T, Hkv, Dk))
     s = load().fix_attn_rotary(
         p, r, None if positions is None else positions.data_ptr(), q.data_ptr(), qs, kp, ks,
         q_out.data_ptr(), None if k is None else k_out.data_ptr(), 1 if inverse else 0,
@@ -459,32 +460,34 @@ def fix_attn_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved
 
 def _page_cache(k_pages, v_pages, g_pages, page_table, seqlens, status, S, index):
     """(PageCache, Hkv, Dk, Dv, scalar gate)."""
-    _tensor("k_pages", k_pages, torch.bfloat16, index)
-    _tensor("v_pages", v_pages, torch.bfloat16, index)
-    _tensor("g_pages", g_pages, torch.float32, index)
-    _tensor("page_table", page_table, torch.int32, index)
-    _tensor("seqlens", seqlens, torch.int32, index)
-    kd, vd, gd = k_pages.shape, v_pages.shape, g_pages.shape
-    _need(len(kd) == 4 and k_pages.is_contiguous(),
-          "k_pages must be a dense [num_pages,page_size,Hkv,Dk]")
-    _need(len(vd) == 4 and vd[:3] == kd[:3] and v_pages.is_contiguous(),
-          "v_pages must be a dense [num_pages,page_size,Hkv,Dv]")
+    _tensor("k_pages", k_pages, _bf16, index)
+    _tensor("v_pages", v_pages, _bf16, index)
+    _tensor("g_pages", g_pages, _f32, index)
+    _tensor("page_table", page_table, _i32, index)
+    _tensor("seqlens", seqlens, _i32, index)
+    kd, vd, gd, td = k_pages.shape, v_pages.shape, g_pages.shape, page_table.shape
+    if len(kd) != 4 or not k_pages.is_contiguous():
+        raise ValueError("k_pages must be a dense [num_pages,page_size,Hkv,Dk]")
+    P, ps, Hkv, Dk = kd
+    if len(vd) != 4 or not v_pages.is_contiguous() or vd[0] != P or vd[1] != ps or vd[2] != Hkv:
+        raise ValueError("v_pages must be a dense [num_pages,page_size,Hkv,Dv]")
+    Dv = vd[3]
     scalar = len(gd) == 3
-    _need(gd == (vd[:3] if scalar else vd) and g_pages.is_contiguous(),
-          "g_pages must be a dense [num_pages,page_size,Hkv,Dv] or [num_pages,page_size,Hkv]")
-    td = page_table.shape
+    if (gd != (P, ps, Hkv) if scalar else gd != vd) or not g_pages.is_contiguous():
+        raise ValueError("g_pages must be a dense [num_pages,page_size,Hkv,Dv] or "
+                         "[num_pages,page_size,Hkv]")
     if len(td) != 2 or td[0] != S or not page_table.is_contiguous():
         raise ValueError(f"page_table must be a dense [{S},max_pages]")
     if seqlens.shape != (S,) or not seqlens.is_contiguous():
         raise ValueError(f"seqlens must be a dense [{S}]")
     sp = None
     if status is not None:
-        _tensor("status", status, torch.int32, index)
+        _tensor("status", status, _i32, index)
         _need(status.numel() == 1, "status must hold one int32")
         sp = status.data_ptr()
-    return (PageCache(kd[1], kd[0], td[1], page_table.data_ptr(), seqlens.data_ptr(),
+    return (PageCache(ps, P, td[1], page_table.data_ptr(), seqlens.data_ptr(),
                       k_pages.data_ptr(), v_pages.data_ptr(), g_pages.data_ptr(), sp),
-            kd[2], kd[3], vd[3], scalar)
+            Hkv, Dk, Dv, scalar)
 
 
 def fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlens,
@@ -506,19 +509,20 @@ def fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlen
         with ctx:
             return fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlens,
                                          cu_seqlens, q, inv_freq, interleaved, return_k, status)
-    _tensor("k", k, torch.bfloat16, index)
-    _tensor("v", v, torch.bfloat16, index)
-    _tensor("g", g, torch.float32, index)
+    _tensor("k", k, _bf16, index)
+    _tensor("v", v, _bf16, index)
+    _tensor("g", g, _f32, index)
     kd, vd, gd = k.shape, v.shape, g.shape
-    _need(len(kd) == 4 and len(vd) == 4 and vd[:3] == kd[:3],
-          "k and v must be [B,T,Hkv,Dk] and [B,T,Hkv,Dv]")
+    if len(kd) != 4 or len(vd) != 4 or vd[0] != kd[0] or vd[1] != kd[1] or vd[2] != kd[2]:
+        raise ValueError("k and v must be [B,T,Hkv,Dk] and [B,T,Hkv,Dv]")
     B, T, Hkv, Dk = kd
     Dv = vd[3]
     scalar = len(gd) == 3
-    _need(gd == (vd[:3] if scalar else vd), "g must be [B,T,Hkv,Dv] or [B,T,Hkv]")
+    if gd != (B, T, Hkv) if scalar else gd != vd:
+        raise ValueError("g must be [B,T,Hkv,Dv] or [B,T,Hkv]")
     Hq, qs, qp = Hkv, 0, None
     if q is not None:
-        _tensor("q", q, torch.bfloat16, index)
+        _tensor("q", q, _bf16, index)
         _need(q.dim() == 4, "q must be [B,T,Hq,Dk]")
         Bq, Tq, Hq, Dkq = q.shape
         _need(Bq == B and Tq == T and Dkq == Dk, "q must have k's B, T and Dk")
@@ -549,7 +553,7 @@ def fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlen
 def _paged_problem(q, k_pages, v_pages, g_pages, page_table, seqlens, scale, eps, y_dtype, o_norm,
                    status):
     index = _cuda_index("q", q)
-    _tensor("q", q, torch.bfloat16, index)
+    _tensor("q", q, _bf16, index)
     _need(q.dim() == 3 and q.is_contiguous(), "q must be a dense [B,Hq,Dk]")
     _need(y_dtype is torch.bfloat16 or y_dtype is torch.float32,
           "y_dtype must be bfloat16 or float32")
@@ -592,10 +596,10 @@ def fix_attn_decode_paged(q, k_pages, v_pages, g_pages, page_table, seqlens, o_n
     _need(o_norm_weight is not None or not o_norm, "o_norm=True needs o_norm_weight")
     wp = zp = None
     if o_norm_weight is not None:
-        _dense("o_norm_weight", o_norm_weight, torch.bfloat16, index, shape[2:])
+        _dense("o_norm_weight", o_norm_weight, _bf16, index, shape[2:])
         wp = o_norm_weight.data_ptr()
     if o_gate is not None:
-        _dense("o_gate", o_gate, torch.bfloat16, index, shape)
+        _dense("o_gate", o_gate, _bf16, index, shape)
         zp = o_gate.data_ptr()
     lib = load()
     if out is None:

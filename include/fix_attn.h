@@ -289,7 +289,9 @@ fix_status fix_attn_append_paged(const fix_attn_problem *p, const fix_attn_page_
  * head dims, scale, eps, y_dtype, FIX_FLAG_NO_NORM / FIX_FLAG_SCALAR_GATE.
  *   q [B,Hq,Dk] bf16, o_norm_weight, o_gate, y as in fix_attn_decode.
  * A sequence of length 0 gives y = 0.  Slots past a sequence's length are
- * never read.  Any Hq/Hkv.  The work is split over the cache on the device by
+ * never read.  Any Hq/Hkv; with C = max_pages * page_size (or 2^31 - 1 if less)
+ * and r = ceil(Hq/Hkv / 16), B * Hkv * r * (C / 16 + 4) must stay below 2^31
+ * (FIX_ERR_SHAPE).  The work is split over the cache on the device by
  * the lengths found there, so a captured call may be replayed with others.
  * The workspace needs no initialisation; calls that may overlap need one
  * each. */
