@@ -82,42 +82,60 @@ __device__ __forceinline__ int paged_tiles(const PagedArgs& a, int b) {
 // Line positions of one unit of n tiles.
 __device__ __forceinline__ int paged_cost(int n) { return n ? n + kUnitCost : 0; }
 
+__device__ __forceinline__ int warp_upto(int x) {      // sum over this lane and those below
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
 // The line over all sequences, for a whole warp: lane i sums a run of K
 // sequences.  (The host refuses sizes whose line could pass 2^31 positions.)
 struct Line {
-  int K;
+  int K, len;            // sequences per lane; the length of the lane's last one
   int mine, upto;        // positions of this lane's run; of the runs up to it
   __device__ __forceinline__ Line(const PagedArgs& a, int upb) {
     const int lane = threadIdx.x & 31;
     K = (a.B + 31) / 32;
-    mine = 0;
+    len = mine = 0;
 #pragma unroll 8
-    for (int i = lane * K; i < min(a.B, (lane + 1) * K); ++i) mine += paged_cost(paged_tiles(a, i));
-    mine *= upb;
-    upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
+    for (int i = lane * K; i < min(a.B, (lane + 1) * K); ++i) {
+      len = paged_len(a, i);
+      mine += paged_cost(tiles_of(len));
     }
+    mine *= upb;
+    upto = warp_upto(mine);
   }
   __device__ __forceinline__ int total() const { return __shfl_sync(0xffffffffu, upto, 31); }
-  // The sequence that holds position pos < total(), its length and where it
+  // The sequence b that holds position pos < total(), its length L and where it
   // starts.
-  __device__ __forceinline__ void find(const PagedArgs& a, int pos, int upb, int* b, int* len,
+  __device__ __forceinline__ void find(const PagedArgs& a, int pos, int upb, int* b, int* L,
                                        int* start) const {
+    const int lane = threadIdx.x & 31;
     const int src = __ffs(__ballot_sync(0xffffffffu, upto > pos)) - 1;
-    int at = __shfl_sync(0xffffffffu, upto - mine, src);
-    int i = src * K;
-    for (;;) {
-      *len = paged_len(a, i);
-      const int t = paged_cost(tiles_of(*len)) * upb;
-      if (pos < at + t || i + 1 >= a.B) break;
-      at += t;
-      ++i;
+    *start = __shfl_sync(0xffffffffu, upto - mine, src);
+    if (K == 1) {
+      *b = src;
+      *L = __shfl_sync(0xffffffffu, len, src);
+      return;
     }
-    *b = i;
-    *start = at;
+    for (int i0 = src * K;; i0 += 32) {                  // within the run, 32 at a time
+      const int i = i0 + lane;
+      const int l = i < min(a.B, (src + 1) * K) ? paged_len(a, i) : 0;
+      const int t = paged_cost(tiles_of(l)) * upb, sum = warp_upto(t);
+      const uint32_t in = __ballot_sync(0xffffffffu, *start + sum > pos);
+      if (in) {
+        const int f = __ffs(in) - 1;
+        *b = i0 + f;
+        *L = __shfl_sync(0xffffffffu, l, f);
+        *start += __shfl_sync(0xffffffffu, sum - t, f);
+        return;
+      }
+      *start += __shfl_sync(0xffffffffu, sum, 31);
+    }
   }
 };
 
@@ -353,7 +371,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
         for (int it = 0; it < Dk / 16; ++it, key += per, src += step)
           copy16(dst + key * kpitch + ((c ^ (key & 7)) << 4), src, true);
       } else {
-#pragma unroll 1
+#pragma unroll 4
         for (int it = 0; it < Dk / 16; ++it, key += per) {
           const uint32_t rr = __shfl_sync(0xffffffffu, row, from + key);
           copy16(dst + key * kpitch + ((c ^ (key & 7)) << 4), a.k + (size_t)rr * Dk + c * 8,
@@ -387,7 +405,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
           }
         }
       } else {
-#pragma unroll 1
+#pragma unroll 4
         for (int it = 0; it < DV / 16; ++it) {
           const int key = it * (32 / CV) + lane / CV;
           const uint32_t rr = __shfl_sync(0xffffffffu, row, from + key);
@@ -395,7 +413,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
                  (there >> key) & 1);
         }
         if constexpr (!SCALAR) {
-#pragma unroll 1
+#pragma unroll 4
           for (int it = 0; it < DV / 8; ++it) {
             const int key = it * (32 / CG) + lane / CG;
             const uint32_t rr = __shfl_sync(0xffffffffu, row, from + key);
