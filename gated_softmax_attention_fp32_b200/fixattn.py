@@ -13,6 +13,7 @@ the pair in a ``torch.autograd.Function`` with the FiX README's argument order
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -408,6 +409,38 @@ def _token_problem(q_heads, k_heads, B, T, Dk, Dv, cu_seqlens, index, scalar=Fal
     return p
 
 
+def _rotary_plan(q, k, inv_freq, cu_seqlens, positions, interleaved, index):
+    """Checks a rotation's arguments: (Problem, Rotation, positions' address)."""
+    _tensor("q", q, _bf16, index)
+    qd = q.shape
+    _need(len(qd) == 4, "q must be [B,T,Hq,Dk]")
+    B, T, Hq, Dk = qd
+    Hkv = Hq
+    if k is not None:
+        _tensor("k", k, _bf16, index)
+        kd = k.shape
+        if len(kd) != 4 or kd[0] != B or kd[1] != T or kd[3] != Dk:
+            raise ValueError("k must be [B,T,Hkv,Dk] with q's B, T and Dk")
+        Hkv = kd[2]
+    r = _rotation(inv_freq, Dk, interleaved, index)
+    p = _token_problem(Hq, Hkv, B, T, Dk, Dk, cu_seqlens, index)
+    if positions is None:
+        return p, r, None
+    _dense("positions", positions, _i32, index, (B, T))
+    return p, r, positions.data_ptr()
+
+
+def _rotate(plan, q, qs, k, ks, q_out, k_out, inverse, index):
+    p, r, positions = plan
+    s = load().fix_attn_rotary(
+        p, r, positions, q.data_ptr(), qs, None if k is None else k.data_ptr(), ks,
+        q_out.data_ptr(), None if k is None else k_out.data_ptr(), 1 if inverse else 0,
+        _raw_stream(index))
+    if s != 0:
+        raise FixStatusError(s, "fix_attn_rotary")
+    return q_out, k_out
+
+
 def fix_attn_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved=False,
                     inverse=False, out=None, stream=None):
     """Rotates q [B,T,Hq,Dk] and k [B,T,Hkv,Dk] (or None) by position: the
@@ -424,38 +457,19 @@ def fix_attn_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved
     if ctx is not None:
         with ctx:
             return fix_attn_rotary(q, k, inv_freq, cu_seqlens, positions, interleaved, inverse, out)
-    _tensor("q", q, _bf16, index)
-    _need(q.dim() == 4, "q must be [B,T,Hq,Dk]")
-    B, T, Hq, Dk = q.shape
-    Hkv, ks, kp = Hq, 0, None
-    if k is not None:
-        _tensor("k", k, _bf16, index)
-        _need(k.dim() == 4, "k must be [B,T,Hkv,Dk]")
-        Bk, Tk, Hkv, Dkk = k.shape
-        _need(Bk == B and Tk == T and Dkk == Dk, "k must have q's B, T and Dk")
-        ks = _token_stride("k", k, Hkv * Dk)
-        kp = k.data_ptr()
-    r = _rotation(inv_freq, Dk, interleaved, index)
-    p = _token_problem(Hq, Hkv, B, T, Dk, Dk, cu_seqlens, index)
-    if positions is not None:
-        _dense("positions", positions, _i32, index, (B, T))
-    qs = _token_stride("q", q, Hq * Dk)
+    plan = _rotary_plan(q, k, inv_freq, cu_seqlens, positions, interleaved, index)
+    qs = _token_stride("q", q, q.shape[2] * q.shape[3])
+    ks = _token_stride("k", k, k.shape[2] * k.shape[3]) if k is not None else 0
     if out is None:
-        q_out = q.new_empty((B, T, Hq, Dk))
-        k_out = k.new_empty((B, T, Hkv, Dk)) if k is not None else None
+        q_out = q.new_empty(q.shape)
+        k_out = k.new_empty(k.shape) if k is not None else None
     else:
         q_out, k_out = out
-        _dense("out[0]", q_out, _bf16, index, (B, T, Hq, Dk))
+        _dense("out[0]", q_out, _bf16, index, q.shape)
         _need((k is None) == (k_out is None), "out[1] goes with k")
         if k is not None:
-            _dense("out[1]", k_out, _bf16, index, (B, T, Hkv, Dk))
-    s = load().fix_attn_rotary(
-        p, r, None if positions is None else positions.data_ptr(), q.data_ptr(), qs, kp, ks,
-        q_out.data_ptr(), None if k is None else k_out.data_ptr(), 1 if inverse else 0,
-        _raw_stream(index))
-    if s != 0:
-        raise FixStatusError(s, "fix_attn_rotary")
-    return q_out, k_out
+            _dense("out[1]", k_out, _bf16, index, k.shape)
+    return _rotate(plan, q, qs, k, ks, q_out, k_out, inverse, index)
 
 
 def _page_cache(k_pages, v_pages, g_pages, page_table, seqlens, status, S, index):
@@ -664,26 +678,46 @@ class _FixAttn(torch.autograd.Function):
         return dq, dk, dv, dg, dw, dz, None, None, None, None, None, None, None
 
 
+def _aligned(t):
+    """A gradient as autograd hands it over, dense and on a 16-byte boundary."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
+
+
 class _FixRotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, inv_freq, cu_seqlens, positions, interleaved, inverse):
+        index = _cuda_index("q", q)
         ctx.save_for_backward(inv_freq, cu_seqlens, positions)
-        ctx.cfg = (interleaved, not inverse)
-        return fix_attn_rotary(q, k, inv_freq, cu_seqlens, positions, interleaved, inverse)
+        ctx.cfg = (interleaved, inverse)
+        with _elsewhere(index, None) or contextlib.nullcontext():
+            plan = ctx.plan = _rotary_plan(q, k, inv_freq, cu_seqlens, positions, interleaved,
+                                           index)
+            return _rotate(plan, q, _token_stride("q", q, q.shape[2] * q.shape[3]), k,
+                           _token_stride("k", k, k.shape[2] * k.shape[3]), q.new_empty(q.shape),
+                           k.new_empty(k.shape), inverse, index)
 
     @staticmethod
     def backward(ctx, dq, dk):
         # the rotation is linear and orthogonal: its gradient is the rotation
-        # back, itself differentiable
-        apply = _FixRotary.apply if torch.is_grad_enabled() else fix_attn_rotary
-        dq, dk = apply(dq.contiguous(), dk.contiguous(), *ctx.saved_tensors, *ctx.cfg)
+        # back (itself differentiable)
+        saved = ctx.saved_tensors            # raises where one was changed since
+        interleaved, inverse = ctx.cfg
+        dq, dk = _aligned(dq), _aligned(dk)
+        if torch.is_grad_enabled():
+            dq, dk = _FixRotary.apply(dq, dk, *saved, interleaved, not inverse)
+        else:
+            dq, dk = _rotate(ctx.plan, dq, 0, dk, 0, dq.new_empty(dq.shape),
+                             dk.new_empty(dk.shape), not inverse, dq.get_device())
         return dq, dk, None, None, None, None, None
 
 
 def fix_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved=False):
     """``fix_attn_rotary`` of q and k, differentiable in both: the rotation
     that a model trains with before ``fix_attn``, the same that
-    ``fix_attn_append_paged`` applies when it serves."""
+    ``fix_attn_append_paged`` applies when it serves.  Forward and backward may
+    be captured into a CUDA graph, as PyTorch's own operations may: not while
+    an uncaptured autograd graph of the same leaves is alive."""
     _need(k is not None, "fix_rotary needs q and k")
     return _FixRotary.apply(q, k, inv_freq, cu_seqlens, positions, bool(interleaved), False)
 

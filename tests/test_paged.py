@@ -880,3 +880,67 @@ def test_decode_paged_all_nan(cuda_lib):
     assert bool(nan[2, :2].all()) and not nan[2, 2:].any() and not nan[3].any()
     check = decode_ref(q[3], *c.tok[3], w, None, 64 ** -0.5, 1e-6, True)
     assert float((y[3] - check).norm() / check.norm()) <= F32_ROW
+
+
+@pytest.mark.gpu
+def test_rotary_gradient_as_autograd_calls_it(cuda_lib):
+    """Gradients that are views off the 16-byte boundary, leaves that are
+    broadcast, a second derivative, inputs changed before the backward, and a
+    captured forward and backward."""
+    gen = torch.Generator().manual_seed(9)
+    B, T, H, D = 2, 6, 2, 32
+    mk = lambda *s: torch.randn(*s, generator=gen).to(bf16)  # noqa: E731
+    q, k, f = mk(B, T, H, D), mk(B, T, H, D), inv_freq(D)
+    pos = [t for _ in range(B) for t in range(T)]
+    ql, kl = q.cuda().requires_grad_(True), k.cuda().requires_grad_(True)
+    fd = f.cuda()
+    flat = mk(B * T * H * D + 1).cuda()
+    off = flat[1:].view(B, T, H, D)                              # 2 bytes off
+    gq, gk = torch.autograd.grad(fixattn.fix_rotary(ql, kl, fd), (ql, kl), (off, off))
+    check_rotated(gq, off.cpu(), pos, f, False, True)
+    check_rotated(gk, off.cpu(), pos, f, False, True)
+    # one head's keys for all heads: the gradient is the sum over the copies
+    one = mk(B, T, 1, D)
+    ol = one.cuda().requires_grad_(True)
+    dk = mk(B, T, H, D)
+    _, kr = fixattn.fix_rotary(ql, ol.expand(B, T, H, D).contiguous(), fd)
+    go, = torch.autograd.grad(kr, ol, dk.cuda())
+    ref, mag = rotate_ref(dk.flatten(0, 1), pos, f, inverse=True)
+    err = (go.double().cpu().flatten(0, 1) - ref.sum(1, keepdim=True)).abs()
+    # a rounding of each summand and one of the sum
+    bar = BF16 * (ref.abs().sum(1, keepdim=True) + ref.sum(1, keepdim=True).abs()) + 1e-6 * mag.sum(1, keepdim=True)
+    assert bool((err <= bar).all())
+    # the gradient is linear in the incoming one, with the rotation itself as derivative
+    d = mk(B, T, H, D).cuda().requires_grad_(True)
+    g1, = torch.autograd.grad(fixattn.fix_rotary(ql, kl, fd)[0], ql, d, create_graph=True)
+    g2, = torch.autograd.grad(g1, d, off)
+    check_rotated(g2, off.cpu(), pos, f)
+    # positions changed between forward and backward
+    positions = torch.zeros(B, T, dtype=torch.int32, device="cuda")
+    qr, kr = fixattn.fix_rotary(ql, kl, fd, positions=positions)
+    positions += 1
+    with pytest.raises(RuntimeError, match="modified"):
+        torch.autograd.grad((qr, kr), (ql, kl), (off, off))
+    # captured, with leaves of its own (PyTorch ties a leaf's accumulation to the stream of the oldest graph
+    # of it that lives: as with any of its operations, the capture fails while an eager one is)
+    ql, kl = q.cuda().requires_grad_(True), k.cuda().requires_grad_(True)
+    dq = mk(B, T, H, D).cuda()
+
+    def step():
+        a, b = fixattn.fix_rotary(ql, kl, fd)
+        return (a, b) + torch.autograd.grad((a, b), (ql, kl), (dq, dq))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    with torch.no_grad():
+        ql.copy_(mk(B, T, H, D))
+        dq.copy_(mk(B, T, H, D))
+    graph.replay()
+    want = step()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
