@@ -740,13 +740,13 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 // there are more units than workers) the workers, each for the cut unit that
 // begins in its span; grid.y: the head blocks' heads, heads_per_cta at a time.
 // A head has warps_per_head warps, each for a run of its pieces, newest first
-// and four loads deep (what it costs is the latency of its loads); channels
-// lie over the lanes.
+// and kDeep pieces at a time (what it costs is the latency of its loads);
+// channels lie over the lanes.
 template <int DV>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     paged_join_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int VPL = DV >= 32 ? DV / 32 : 1;
-  constexpr int kDeep = 4;
+  constexpr int kDeep = 4;      // 8 is no faster, and slower for few pieces
   __shared__ float so[kJoinWarps][DV], stot[kJoinWarps][DV], sml[kJoinWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int upb = a.Hkv * a.nhb;
@@ -905,9 +905,9 @@ static fix_status paged_launch(const PagedArgs& a, const PagedPlan& pl, cudaStre
   auto* kernel = paged_decode_kernel<DV, NT, SCALAR>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), pl.smem)) return FIX_ERR_CUDA;
   FIX_PAGED_TRY(OverlappedLaunch(dim3(pl.ctas), kPagedWarps * 32, pl.smem, st).run(kernel, a));
-  return OverlappedLaunch(dim3(pl.jobs, (a.hpb + a.heads_per_cta - 1) / a.heads_per_cta),
-                          a.heads_per_cta * a.warps_per_head * 32, 0, st)
-      .run(paged_join_kernel<DV>, a);
+  const OverlappedLaunch join(dim3(pl.jobs, (a.hpb + a.heads_per_cta - 1) / a.heads_per_cta),
+                              a.heads_per_cta * a.warps_per_head * 32, 0, st);
+  return join.run(paged_join_kernel<DV>, a);
 }
 
 template <int DV>

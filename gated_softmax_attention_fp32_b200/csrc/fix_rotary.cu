@@ -141,6 +141,10 @@ __global__ void __launch_bounds__(kTokWarps * 32) token_kernel(const __grid_cons
     }
   }
 
+  const bool gates = a.scalar && blockIdx.y == 0;   // one float per kv head
+  const float* gn = a.g + (long long)n * a.gs;
+  const float g0 = gates && lane < a.Hkv ? gn[lane] : 0.f;
+
   // the token's position, and its row in the pools
   int b = 0;
   long long t = 0, len = 0, pos = -1, row = -1;
@@ -205,8 +209,11 @@ __global__ void __launch_bounds__(kTokWarps * 32) token_kernel(const __grid_cons
       *reinterpret_cast<uint4*>(d + to1) = y[i];
     }
   }
-  if (a.scalar && row >= 0 && blockIdx.y == 0)    // one float per kv head
-    for (int h = lane; h < a.Hkv; h += 32) a.g_pages[row * a.Hkv + h] = a.g[n * a.gs + h];
+  if (gates && row >= 0) {
+    float* to = a.g_pages + row * a.Hkv;
+    if (lane < a.Hkv) to[lane] = g0;
+    for (int h = lane + 32; h < a.Hkv; h += 32) to[h] = gn[h];
+  }
 }
 
 static bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -296,7 +303,7 @@ extern "C" fix_status fix_attn_rotary(const fix_attn_problem* p, const fix_attn_
   FIX_ROT_TRY(token_stride(k_stride, (long long)d.Hkv * d.Dk, 8, &a.ks));
   a.N = d.N; a.T = d.T; a.nseq = d.nseq; a.cu = p->cu_seqlens;
   a.positions = positions;
-  a.Hq = d.Hq; a.Hkv = d.Hkv; a.Dk = d.Dk; a.Dv = d.Dv; a.scalar = d.scalar_gate;
+  a.Hq = d.Hq; a.Hkv = d.Hkv; a.Dk = d.Dk; a.Dv = d.Dv;
   a.rot = r->rot_dim; a.interleaved = r->interleaved; a.inverse = inverse;
   a.inv_freq = r->inv_freq;
   a.q = static_cast<const __nv_bfloat16*>(q);
