@@ -794,11 +794,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       for (int e = 0; e < VPL; ++e) o[e] *= f0;
 #pragma unroll
       for (int d = 0; d < kDeep; ++d) {
+        // a piece without weight adds nothing, whatever the gates: those of the
+        // sequence's first token, which no decay uses, are in `after` by then
         const float f = ex2(pm[d] - ref);
         l += f * pl[d];
 #pragma unroll
         for (int e = 0; e < VPL; ++e) {
-          o[e] += f * x[d][e] * ex2(after[e]);
+          if (pl[d] != 0.f) o[e] += f * x[d][e] * ex2(after[e]);
           after[e] += t[d][e];
         }
       }
@@ -821,12 +823,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   for (int e = 0; e < VPL; ++e) o[e] = after[e] = 0.f;
 #pragma unroll 4
   for (int i = wph - 1; i >= 0; --i) {
-    const float f = ex2(sml[warp + i][0] - M);
-    l += f * sml[warp + i][1];
+    const float f = ex2(sml[warp + i][0] - M), li = sml[warp + i][1];
+    l += f * li;
     if (!live) continue;
 #pragma unroll
     for (int e = 0; e < VPL; ++e) {
-      o[e] += f * so[warp + i][c0 + e] * ex2(after[e]);
+      if (li != 0.f) o[e] += f * so[warp + i][c0 + e] * ex2(after[e]);
       after[e] += stot[warp + i][c0 + e];
     }
   }

@@ -216,7 +216,9 @@ __global__ void __launch_bounds__(kTokWarps * 32) token_kernel(const __grid_cons
   }
 }
 
-static bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+static bool misaligned(const void* p, unsigned bytes = 16) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
+}
 
 // A token stride in elements: 0 selects the dense one.
 static fix_status token_stride(int64_t given, long long dense, int multiple, long long* out) {
@@ -243,7 +245,7 @@ static fix_status token_dims(const fix_attn_problem* p, Dims* d) {
 
 static fix_status check_rotation(const fix_attn_rotation* r, const Dims& d) {
   if (!r->inv_freq) return FIX_ERR_NULL;
-  if (misaligned(r->inv_freq)) return FIX_ERR_ALIGN;
+  if (misaligned(r->inv_freq, 4)) return FIX_ERR_ALIGN;
   if (r->rot_dim < 16 || r->rot_dim > d.Dk || r->rot_dim % 16) return FIX_ERR_SHAPE;
   return FIX_OK;
 }
@@ -253,10 +255,10 @@ fix_status validate_cache(const fix_attn_page_cache* c, const Dims& d) {
   if (c->page_size < 1 || c->num_pages < 1 || c->max_pages < 1) return FIX_ERR_SHAPE;
   if ((unsigned long long)c->num_pages * c->page_size >= (1ULL << 32) / d.Hkv) return FIX_ERR_SHAPE;
   if (!c->page_table || !c->seqlens || !c->k_pages || !c->v_pages || !c->g_pages) return FIX_ERR_NULL;
-  for (const void* x : {(const void*)c->page_table, (const void*)c->seqlens, (const void*)c->k_pages,
-                        (const void*)c->v_pages, (const void*)c->g_pages})
+  for (const void* x : {(const void*)c->k_pages, (const void*)c->v_pages, (const void*)c->g_pages})
     if (misaligned(x)) return FIX_ERR_ALIGN;
-  if (reinterpret_cast<uintptr_t>(c->status) & 3u) return FIX_ERR_ALIGN;
+  for (const void* x : {(const void*)c->page_table, (const void*)c->seqlens, (const void*)c->status})
+    if (misaligned(x, 4)) return FIX_ERR_ALIGN;
   return FIX_OK;
 }
 
@@ -295,9 +297,9 @@ extern "C" fix_status fix_attn_rotary(const fix_attn_problem* p, const fix_attn_
   if (d.N == 0) return FIX_OK;
   if (!r || !q || !q_out || (!k) != (!k_out)) return FIX_ERR_NULL;
   FIX_ROT_TRY(check_rotation(r, d));
-  for (const void* x : {q, k, (const void*)q_out, (const void*)k_out, (const void*)p->cu_seqlens})
+  for (const void* x : {q, k, (const void*)q_out, (const void*)k_out})
     if (misaligned(x)) return FIX_ERR_ALIGN;
-  if (reinterpret_cast<uintptr_t>(positions) & 3u) return FIX_ERR_ALIGN;
+  if (misaligned(positions, 4) || misaligned(p->cu_seqlens, 8)) return FIX_ERR_ALIGN;
   TokenArgs a{};
   FIX_ROT_TRY(token_stride(q_stride, (long long)d.Hq * d.Dk, 8, &a.qs));
   FIX_ROT_TRY(token_stride(k_stride, (long long)d.Hkv * d.Dk, 8, &a.ks));
@@ -327,9 +329,9 @@ extern "C" fix_status fix_attn_append_paged(const fix_attn_problem* p, const fix
   FIX_ROT_TRY(validate_cache(c, d));
   if (!k || !v || !g || (!q) != (!q_out) || (!r && (q || k_out))) return FIX_ERR_NULL;
   if (r) FIX_ROT_TRY(check_rotation(r, d));
-  for (const void* x : {q, k, v, (const void*)q_out, (const void*)k_out, (const void*)p->cu_seqlens})
+  for (const void* x : {q, k, v, (const void*)q_out, (const void*)k_out})
     if (misaligned(x)) return FIX_ERR_ALIGN;
-  if (reinterpret_cast<uintptr_t>(g) & (d.scalar_gate ? 3u : 15u)) return FIX_ERR_ALIGN;
+  if (misaligned(g, d.scalar_gate ? 4 : 16) || misaligned(p->cu_seqlens, 8)) return FIX_ERR_ALIGN;
   TokenArgs a{};
   FIX_ROT_TRY(token_stride(q_stride, (long long)d.Hq * d.Dk, 8, &a.qs));
   FIX_ROT_TRY(token_stride(k_stride, (long long)d.Hkv * d.Dk, 8, &a.ks));

@@ -208,7 +208,7 @@ fix_status fix_attn_decode(const fix_attn_problem *p, const int32_t *seqlens, co
  * abstract calls the gate complementary to a rotation of queries and keys,
  * which the caller applies before the attention.) */
 typedef struct {
-  const float *inv_freq;  /* device f32 [rot_dim/2], 16-byte aligned          */
+  const float *inv_freq;  /* device f32 [rot_dim/2]                           */
   int32_t rot_dim;        /* rotated channels: a multiple of 16 in [16, Dk]   */
   int32_t interleaved;    /* 0: pairs (i, i + rot_dim/2); 1: (2i, 2i + 1)      */
 } fix_attn_rotation;
@@ -238,7 +238,8 @@ fix_status fix_attn_rotary(const fix_attn_problem *p, const fix_attn_rotation *r
  *   g_pages [num_pages,page_size,Hkv,Dv] f32 ([num_pages,page_size,Hkv] with
  *           FIX_FLAG_SCALAR_GATE).
  * num_pages * page_size * Hkv must stay below 2^32.  Table entries that no
- * token needs are not used (any value may stand there). */
+ * token needs are not used (any value may stand there).  The pools are 16-byte
+ * aligned; integer arrays (and inv_freq above) only as their type is. */
 typedef struct {
   int32_t page_size;          /* tokens per page, >= 1                         */
   int32_t num_pages;          /* pages in the pools                            */
@@ -288,8 +289,10 @@ fix_status fix_attn_append_paged(const fix_attn_problem *p, const fix_attn_page_
  * included; keys rotated where q is).  problem: batch = B, seqlen = 1, heads,
  * head dims, scale, eps, y_dtype, FIX_FLAG_NO_NORM / FIX_FLAG_SCALAR_GATE.
  *   q [B,Hq,Dk] bf16, o_norm_weight, o_gate, y as in fix_attn_decode.
- * A sequence of length 0 gives y = 0.  Slots past a sequence's length are
- * never read.  Any Hq/Hkv; with C = max_pages * page_size (or 2^31 - 1 if less)
+ * A sequence of length 0, or without a finite logit, gives y = 0.  Slots past
+ * a sequence's length are never read.  g should be <= 0; positive gates are
+ * computed the same way while exp of their sum over any run of tokens stays
+ * inside the float32 range.  Any Hq/Hkv; with C = max_pages * page_size (or 2^31 - 1 if less)
  * and r = ceil(Hq/Hkv / 16), B * Hkv * r * (C / 16 + 4) must stay below 2^31
  * (FIX_ERR_SHAPE).  The work is split over the cache on the device by
  * the lengths found there, so a captured call may be replayed with others.

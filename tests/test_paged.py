@@ -176,12 +176,12 @@ NULL, SHAPE, HEAD, GQA, CU, ALIGN, WS = 1, 2, 3, 4, 5, 6, 7
     (dict(num_seqs=2), {}, {}, CU),
     (dict(cu_seqlens=A, num_seqs=2), {}, {}, SHAPE),          # packed wants batch 1
     (dict(cu_seqlens=A, batch=1), {}, {}, CU),                # no sequence count
-    (dict(cu_seqlens=A + 8, batch=1, num_seqs=2), {}, {}, ALIGN),
+    (dict(cu_seqlens=A + 4, batch=1, num_seqs=2), {}, {}, ALIGN),
     ({}, dict(rot_dim=24), {}, SHAPE),
     ({}, dict(rot_dim=0), {}, SHAPE),
     ({}, dict(rot_dim=128), {}, SHAPE),
     ({}, dict(inv_freq=None), {}, NULL),
-    ({}, dict(inv_freq=A + 4), {}, ALIGN),
+    ({}, dict(inv_freq=A + 2), {}, ALIGN),
     ({}, {}, dict(q=None), NULL),
     ({}, {}, dict(q_out=None), NULL),
     ({}, {}, dict(k_out=None), NULL),
@@ -205,7 +205,7 @@ BAD_CACHES = [
     (dict(num_pages=1 << 20, page_size=1 << 12), SHAPE),      # rows beyond 32 bits
     (dict(page_table=None), NULL), (dict(seqlens=None), NULL), (dict(k_pages=None), NULL),
     (dict(v_pages=None), NULL), (dict(g_pages=None), NULL),
-    (dict(page_table=A + 4), ALIGN), (dict(k_pages=A + 2), ALIGN), (dict(g_pages=A + 8), ALIGN),
+    (dict(page_table=A + 2), ALIGN), (dict(k_pages=A + 2), ALIGN), (dict(g_pages=A + 8), ALIGN),
     (dict(status=A + 1), ALIGN),
 ]
 
@@ -944,3 +944,27 @@ def test_rotary_gradient_as_autograd_calls_it(cuda_lib):
     graph.replay()
     want = step()
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.gpu
+def test_integer_arrays_at_any_offset_and_the_unused_first_gate(cuda_lib):
+    """Lengths, tables and sequence starts that are slices of larger buffers;
+    and the gate of a sequence's first token, which no decay uses, as NaN."""
+    lens, new = [300, 41, 5000], [1, 0, 2]
+    c = Cache(lens, 2, 64, 64, 16, seed=71, gate=lambda x: -1e-3 * x.abs())
+    for b in range(3):
+        c.g[int(c.table[b, 0]), 0] = NAN
+    kp, vp, gp, table, seqlens = c.cuda()
+    q, w, _ = decode_inputs(3, 6, 64, 64, 72)
+    ints = torch.cat((torch.zeros(1, dtype=torch.int32).cuda(), seqlens))
+    tab = torch.cat((torch.zeros(3, dtype=torch.int32).cuda(), table.flatten()))
+    args = (kp, vp, gp, tab[3:].view(table.shape), ints[1:])
+    y = fixattn.fix_attn_decode_paged(q.cuda(), *args, w.cuda(), y_dtype=torch.float32)
+    check_decode(y, c, q, w, None)
+    cu = torch.tensor([7, 0, 1, 1, 3], dtype=torch.int64).cuda()[1:]
+    f = torch.cat((torch.zeros(1), inv_freq(64))).cuda()[1:]
+    x = torch.randn(1, 3, 2, 64, generator=torch.Generator().manual_seed(5)).to(bf16).cuda()
+    fixattn.fix_attn_append_paged(x, x, x.float(), *args, cu_seqlens=cu, inv_freq=f)
+    pos = [lens[0] - 1, lens[2] - 2, lens[2] - 1]
+    got = torch.stack([kp[int(table[b, p // 16]), p % 16] for b, p in zip((0, 2, 2), pos)])
+    check_rotated(got, x.cpu(), pos, inv_freq(64))
