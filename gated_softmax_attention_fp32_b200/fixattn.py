@@ -347,6 +347,11 @@ def _dense(name, t, dtype, index, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _dense_like(t):
+    """An uninitialised dense tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _token_stride(name, t, inner):
     """Elements between consecutive tokens of a [B,T,...] tensor whose inner
     dims (``inner`` elements) are dense: a dense tensor or a slice of a fused
@@ -461,8 +466,8 @@ def fix_attn_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved
     qs = _token_stride("q", q, q.shape[2] * q.shape[3])
     ks = _token_stride("k", k, k.shape[2] * k.shape[3]) if k is not None else 0
     if out is None:
-        q_out = q.new_empty(q.shape)
-        k_out = k.new_empty(k.shape) if k is not None else None
+        q_out = _dense_like(q)
+        k_out = _dense_like(k) if k is not None else None
     else:
         q_out, k_out = out
         _dense("out[0]", q_out, _bf16, index, q.shape)
@@ -474,11 +479,19 @@ def fix_attn_rotary(q, k, inv_freq, cu_seqlens=None, positions=None, interleaved
 
 def _page_cache(k_pages, v_pages, g_pages, page_table, seqlens, status, S, index):
     """(PageCache, Hkv, Dk, Dv, scalar gate)."""
-    _tensor("k_pages", k_pages, _bf16, index)
-    _tensor("v_pages", v_pages, _bf16, index)
-    _tensor("g_pages", g_pages, _f32, index)
-    _tensor("page_table", page_table, _i32, index)
-    _tensor("seqlens", seqlens, _i32, index)
+    try:
+        right = (k_pages.dtype is _bf16 and v_pages.dtype is _bf16 and g_pages.dtype is _f32
+                 and page_table.dtype is _i32 and seqlens.dtype is _i32
+                 and k_pages.get_device() == v_pages.get_device() == g_pages.get_device()
+                 == page_table.get_device() == seqlens.get_device() == index)
+    except AttributeError:
+        right = False
+    if not right:
+        _tensor("k_pages", k_pages, _bf16, index)
+        _tensor("v_pages", v_pages, _bf16, index)
+        _tensor("g_pages", g_pages, _f32, index)
+        _tensor("page_table", page_table, _i32, index)
+        _tensor("seqlens", seqlens, _i32, index)
     kd, vd, gd, td = k_pages.shape, v_pages.shape, g_pages.shape, page_table.shape
     if len(kd) != 4 or not k_pages.is_contiguous():
         raise ValueError("k_pages must be a dense [num_pages,page_size,Hkv,Dk]")
@@ -523,9 +536,15 @@ def fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlen
         with ctx:
             return fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlens,
                                          cu_seqlens, q, inv_freq, interleaved, return_k, status)
-    _tensor("k", k, _bf16, index)
-    _tensor("v", v, _bf16, index)
-    _tensor("g", g, _f32, index)
+    try:
+        right = (k.dtype is _bf16 and v.dtype is _bf16 and g.dtype is _f32
+                 and v.get_device() == g.get_device() == index)
+    except AttributeError:
+        right = False
+    if not right:
+        _tensor("k", k, _bf16, index)
+        _tensor("v", v, _bf16, index)
+        _tensor("g", g, _f32, index)
     kd, vd, gd = k.shape, v.shape, g.shape
     if len(kd) != 4 or len(vd) != 4 or vd[0] != kd[0] or vd[1] != kd[1] or vd[2] != kd[2]:
         raise ValueError("k and v must be [B,T,Hkv,Dk] and [B,T,Hkv,Dv]")
@@ -540,7 +559,7 @@ def fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlen
         _need(q.dim() == 4, "q must be [B,T,Hq,Dk]")
         Bq, Tq, Hq, Dkq = q.shape
         _need(Bq == B and Tq == T and Dkq == Dk, "q must have k's B, T and Dk")
-        qs = _token_stride("q", q, Hq * Dk)
+        qs = 0 if q.is_contiguous() else _token_stride("q", q, Hq * Dk)
         qp = q.data_ptr()
     _need(inv_freq is not None or (q is None and not return_k),
           "q and return_k go with inv_freq")
@@ -550,11 +569,11 @@ def fix_attn_append_paged(k, v, g, k_pages, v_pages, g_pages, page_table, seqlen
     _need(Hp == Hkv and Dkp == Dk and Dvp == Dv and sp == scalar,
           "the pages must have the tokens' heads, dims and gate")
     r = _rotation(inv_freq, Dk, interleaved, index) if inv_freq is not None else None
-    ks = _token_stride("k", k, Hkv * Dk)
-    vs = _token_stride("v", v, Hkv * Dv)
-    gs = _token_stride("g", g, Hkv if scalar else Hkv * Dv)
-    q_out = q.new_empty((B, T, Hq, Dk)) if q is not None else None
-    k_out = k.new_empty((B, T, Hkv, Dk)) if return_k else None
+    ks = 0 if k.is_contiguous() else _token_stride("k", k, Hkv * Dk)    # 0: dense
+    vs = 0 if v.is_contiguous() else _token_stride("v", v, Hkv * Dv)
+    gs = 0 if g.is_contiguous() else _token_stride("g", g, Hkv if scalar else Hkv * Dv)
+    q_out = _dense_like(q) if q is not None else None
+    k_out = _dense_like(k) if return_k else None
     s = load().fix_attn_append_paged(
         p, c, r, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), gs,
         None if q_out is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
@@ -694,8 +713,8 @@ class _FixRotary(torch.autograd.Function):
             plan = ctx.plan = _rotary_plan(q, k, inv_freq, cu_seqlens, positions, interleaved,
                                            index)
             return _rotate(plan, q, _token_stride("q", q, q.shape[2] * q.shape[3]), k,
-                           _token_stride("k", k, k.shape[2] * k.shape[3]), q.new_empty(q.shape),
-                           k.new_empty(k.shape), inverse, index)
+                           _token_stride("k", k, k.shape[2] * k.shape[3]), _dense_like(q),
+                           _dense_like(k), inverse, index)
 
     @staticmethod
     def backward(ctx, dq, dk):
@@ -707,8 +726,8 @@ class _FixRotary(torch.autograd.Function):
         if torch.is_grad_enabled():
             dq, dk = _FixRotary.apply(dq, dk, *saved, interleaved, not inverse)
         else:
-            dq, dk = _rotate(ctx.plan, dq, 0, dk, 0, dq.new_empty(dq.shape),
-                             dk.new_empty(dk.shape), not inverse, dq.get_device())
+            dq, dk = _rotate(ctx.plan, dq, 0, dk, 0, _dense_like(dq), _dense_like(dk),
+                             not inverse, dq.get_device())
         return dq, dk, None, None, None, None, None
 
 
