@@ -31,6 +31,8 @@
 // parts each (11 bits and more), three products: about 2^-21.  Scalar gate:
 // V stays bf16, D goes to P, which is split into three bf16 parts (24 bits).
 // Gate sums are kept in units of log 2.
+#include <type_traits>
+
 #include "fix_internal.h"
 
 #define FIX_PAGED_TRY(expr)           \
@@ -165,6 +167,12 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
                : "r"(addr)
                : "memory");
 }
+__device__ __forceinline__ void ldsm2(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
+               : "=r"(r[0]), "=r"(r[1])
+               : "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -203,6 +211,39 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
 }
 
+template <int N>
+__device__ __forceinline__ void lds_n(uint32_t addr, float* x) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                 : "r"(addr)
+                 : "memory");
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "r"(addr) : "memory");
+  else
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[0]) : "r"(addr) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void sts_n(uint32_t addr, const float* x) {
+  if constexpr (N == 4)
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(x[0]), "f"(x[1]),
+                 "f"(x[2]), "f"(x[3])
+                 : "memory");
+  else if constexpr (N == 2)
+    asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(x[0]), "f"(x[1]) : "memory");
+  else
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x[0]) : "memory");
+}
+
+// Tiles lie in rows of keys (pitch a multiple of 128 bytes), 16-byte chunk c of
+// key s at chunk c ^ (s % 8), so that matrix loads and the gates' reads meet no
+// bank conflicts.  With `addr` that of chunk c0 in its row, the chunk c0 + c
+// (c0 and c without a bit in common) is at chunk_at(addr, c): one xor with a
+// constant for what lies within 128 bytes, the rest a constant offset.
+__device__ __forceinline__ constexpr uint32_t chunk_at(uint32_t addr, int c) {
+  return (addr ^ ((c & 7) << 4)) + (c >> 3) * 128;
+}
+
 // Bytes of one warp's shared memory.
 __host__ __device__ constexpr int row_pitch(int bytes) { return bytes < 128 ? 128 : bytes; }
 template <int DV, bool SCALAR>
@@ -211,7 +252,7 @@ struct Ring {
   static constexpr int kVPitch = row_pitch(DV * 2);
   static constexpr int kGPitch = row_pitch(DV * 4);
   static constexpr int kV = kTileKeys * kVPitch;
-  static constexpr int kG = SCALAR ? 64 : kTileKeys * kGPitch;
+  static constexpr int kG = SCALAR ? 128 : kTileKeys * kGPitch;
   __host__ __device__ static int stage(int Dk) { return kTileKeys * row_pitch(Dk * 2) + kV + kG; }
   __host__ __device__ static int warp_bytes(int Dk, int nt) {
     return (kStages * stage(Dk) + nt * 8 * (Dk * 2 + 16) + 127) / 128 * 128;
@@ -270,7 +311,8 @@ __device__ __forceinline__ float row_factor(const PagedArgs& a, const float* o, 
   return 1.f / sqrtf(warp_sum(sq) / (float)DV + a.eps);
 }
 
-template <int DV, int NT, bool SCALAR>
+// SAME: Dk == DV, known at compile time.
+template <int DV, int NT, bool SCALAR, bool SAME>
 __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
     paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   using R = Ring<DV, SCALAR>;
@@ -279,7 +321,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
   constexpr int VPL = DV >= 32 ? DV / 32 : 1;      // channels per lane where lanes span a row
   extern __shared__ __align__(128) char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int Dk = a.Dk;
+  const int Dk = SAME ? DV : a.Dk;
   const int kpitch = row_pitch(Dk * 2), qpitch = Dk * 2 + 16;
   char* mine = smem + (size_t)warp * R::warp_bytes(Dk, NT);
   const uint32_t ring = smem_addr(mine);
@@ -301,11 +343,17 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 
   // lane roles
   const int j = lane & 3, r8 = lane & 7;
-  const uint32_t kaddr = (uint32_t)(r8 + ((lane >> 3) & 1) * 8) * kpitch;
-  const int kchunk = lane >> 4;
-  const uint32_t vaddr = (uint32_t)(r8 + (lane >> 4) * 8) * R::kVPitch;
-  const int vchunk = (lane >> 3) & 1;
+  const uint32_t kaddr = (r8 + ((lane >> 3) & 1) * 8) * kpitch + (((lane >> 4) ^ r8) << 4);
+  const uint32_t vaddr =
+      (r8 + (lane >> 4) * 8) * R::kVPitch + ((((lane >> 3) & 1) ^ r8) << 4);
+  const uint32_t qaddr = smem_addr(sq) + r8 * qpitch + (lane >> 3) * 16;
   const int key0 = lane >> 2;                               // and key0 + 8: the S rows
+  // gates: of key 2 j and key 2 j + 1, chunk lane / 16, where V' is formed; a
+  // lane's own channels of key 0 where the decays are
+  const uint32_t gpair0 = 2 * j * R::kGPitch + ((lane >> 2) & 3) * 4 + (((lane >> 4) ^ (2 * j)) << 4);
+  const uint32_t gpair1 =
+      (2 * j + 1) * R::kGPitch + ((lane >> 2) & 3) * 4 + (((lane >> 4) ^ (2 * j + 1)) << 4);
+  const uint32_t gmine = lane * VPL * 4;
   const int kshift = 31 - __clz(Dk / 8);
   const bool whole_pages = a.page_size % kTileKeys == 0;    // a tile lies in one page
 
@@ -353,77 +401,50 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
         page = fetch((tile >> 1) - 1);
       }
     };
-    // Tiles go to shared memory in rows of keys, 16-byte chunk c of key s at
-    // chunk c ^ (s % 8): matrix loads and the gates' reads meet no conflicts.
-    // A full tile of one page has evenly spaced rows; keys that are not there
-    // are filled with zeros.
-    auto copy_k = [&](int stage, int tile) {
-      const int from = (tile & 1) * 16;    // lane of the tile's first key
+    // Copies N rows of a tile, CPR 16-byte chunks each, from a pool.  A full tile
+    // of one page has evenly spaced rows; keys that are not there are filled
+    // with zeros.
+    auto copy_rows = [&](uint32_t dst, const void* pool, int tile, auto cpr_, int pitch) {
+      constexpr int kFixed = decltype(cpr_)::value;         // chunks per row, 0: Dk / 8
+      const int from = (tile & 1) * 16;                     // lane of the tile's first key
       const uint32_t there = mask >> from & 0xffffu;
-      const uint32_t dst = ring + stage * stage_bytes;
-      const int c = lane & ((1 << kshift) - 1), per = 32 >> kshift;
-      int key = lane >> kshift;
+      const int shift = kFixed ? 0 : kshift;
+      const int cpr = kFixed ? kFixed : 1 << shift, per = 32 / cpr;
+      const int key = lane / cpr, c = lane % cpr;           // and keys per, 2 per, .. further
+      const uint32_t d = dst + key * pitch + ((c ^ (key & 7)) << 4);
       if (whole_pages && there == 0xffffu) {
-        const __nv_bfloat16* src =
-            a.k + (size_t)(__shfl_sync(0xffffffffu, row, from) + key * a.Hkv) * Dk + c * 8;
-        const size_t step = (size_t)per * a.Hkv * Dk;
-#pragma unroll 8
-        for (int it = 0; it < Dk / 16; ++it, key += per, src += step)
-          copy16(dst + key * kpitch + ((c ^ (key & 7)) << 4), src, true);
+        const uint32_t r0 = __shfl_sync(0xffffffffu, row, from) + key * a.Hkv;
+        const char* src = static_cast<const char*>(pool) + (size_t)r0 * (cpr * 16) + c * 16;
+        const uint32_t stride = a.Hkv * cpr * 16;
+#pragma unroll
+        for (int it = 0; it < (kFixed ? kFixed / 2 : 8); ++it) {
+          if (!kFixed && it >= cpr / 2) break;
+          copy16(chunk_at(d, (it * per) & 7) + it * per * pitch,
+                 src + (size_t)stride * (uint32_t)(it * per), true);
+        }
       } else {
 #pragma unroll 4
-        for (int it = 0; it < Dk / 16; ++it, key += per) {
-          const uint32_t rr = __shfl_sync(0xffffffffu, row, from + key);
-          copy16(dst + key * kpitch + ((c ^ (key & 7)) << 4), a.k + (size_t)rr * Dk + c * 8,
-                 (there >> key) & 1);
+        for (int it = 0; it < cpr / 2; ++it) {
+          const int k = key + it * per;
+          const uint32_t rr = __shfl_sync(0xffffffffu, row, from + k);
+          copy16(chunk_at(d, (it * per) & 7) + it * per * pitch,
+                 static_cast<const char*>(pool) + (size_t)rr * (cpr * 16) + c * 16, there >> k & 1);
         }
       }
     };
+    auto copy_k = [&](int stage, int tile) {
+      copy_rows(ring + stage * stage_bytes, a.k, tile,
+                std::integral_constant<int, SAME ? DV / 8 : 0>{}, kpitch);
+    };
     auto copy_vg = [&](int stage, int tile) {
-      const int from = (tile & 1) * 16;
-      const uint32_t there = mask >> from & 0xffffu;
       const uint32_t dst = ring + stage * stage_bytes + kTileKeys * kpitch;
-      const uint32_t gdst = dst + R::kV;
-      constexpr int CV = DV / 8, CG = DV / 4;               // chunks per row
-      const int vc = lane % CV, gc = lane % CG;
-      if (whole_pages && there == 0xffffu) {
-        const uint32_t row0 = __shfl_sync(0xffffffffu, row, from);
-        const __nv_bfloat16* src = a.v + (size_t)(row0 + (lane / CV) * a.Hkv) * DV + vc * 8;
-        const size_t vstep = (size_t)(32 / CV) * a.Hkv * DV;
-#pragma unroll
-        for (int it = 0; it < DV / 16; ++it, src += vstep) {
-          const int key = it * (32 / CV) + lane / CV;
-          copy16(dst + key * R::kVPitch + ((vc ^ (key & 7)) << 4), src, true);
-        }
-        if constexpr (!SCALAR) {
-          const float* gs = a.g + (size_t)(row0 + (lane / CG) * a.Hkv) * DV + gc * 4;
-          const size_t gstep = (size_t)(32 / CG) * a.Hkv * DV;
-#pragma unroll
-          for (int it = 0; it < DV / 8; ++it, gs += gstep) {
-            const int key = it * (32 / CG) + lane / CG;
-            copy16(gdst + key * R::kGPitch + ((gc ^ (key & 7)) << 4), gs, true);
-          }
-        }
+      copy_rows(dst, a.v, tile, std::integral_constant<int, DV / 8>{}, R::kVPitch);
+      if constexpr (SCALAR) {
+        if ((lane & 16) == (tile & 1) * 16)
+          copy4(dst + R::kV + (lane & 15) * 4, a.g + row, mask >> lane & 1);
       } else {
-#pragma unroll 4
-        for (int it = 0; it < DV / 16; ++it) {
-          const int key = it * (32 / CV) + lane / CV;
-          const uint32_t rr = __shfl_sync(0xffffffffu, row, from + key);
-          copy16(dst + key * R::kVPitch + ((vc ^ (key & 7)) << 4), a.v + (size_t)rr * DV + vc * 8,
-                 (there >> key) & 1);
-        }
-        if constexpr (!SCALAR) {
-#pragma unroll 4
-          for (int it = 0; it < DV / 8; ++it) {
-            const int key = it * (32 / CG) + lane / CG;
-            const uint32_t rr = __shfl_sync(0xffffffffu, row, from + key);
-            copy16(gdst + key * R::kGPitch + ((gc ^ (key & 7)) << 4), a.g + (size_t)rr * DV + gc * 4,
-                   (there >> key) & 1);
-          }
-        }
+        copy_rows(dst + R::kV, a.g, tile, std::integral_constant<int, DV / 4>{}, R::kGPitch);
       }
-      if constexpr (SCALAR)
-        if ((lane & 16) == from) copy4(gdst + (lane & 15) * 4, a.g + row, mask >> lane & 1);
     };
 
     uint32_t masks[ST];
@@ -479,15 +500,19 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
-#pragma unroll 8
-      for (int ks = 0; ks < Dk / 16; ++ks) {
-        uint32_t ka[4];
-        ldsm4(at + kaddr + (((ks * 2 + kchunk) ^ r8) << 4), ka);
+#pragma unroll
+      for (int ks = 0; ks < (SAME ? (DV + 31) / 32 : 4); ++ks) {       // 32 channels at a time
+        if (!SAME && ks * 32 >= Dk) break;
+        uint32_t ka[2][4], qf[NT][4];
+        ldsm4(chunk_at(at + kaddr, 4 * ks), ka[0]);
+        if (Dk > 16) ldsm4(chunk_at(at + kaddr, 4 * ks + 2), ka[1]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const char* qp = sq + (t * 8 + (lane >> 2)) * qpitch + ks * 32 + j * 4;
-          mma_bf16(s[t], ka, *reinterpret_cast<const uint32_t*>(qp),
-                   *reinterpret_cast<const uint32_t*>(qp + 16));
+          const uint32_t qp = qaddr + t * 8 * qpitch + ks * 64;
+          if (Dk > 16) ldsm4(qp, qf[t]);
+          else ldsm2(qp, qf[t]);
+          mma_bf16(s[t], ka[0], qf[t][0], qf[t][1]);
+          if (Dk > 16) mma_bf16(s[t], ka[1], qf[t][2], qf[t][3]);
         }
       }
       __syncwarp();
@@ -537,11 +562,12 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 
       cp_async_wait<2 * ST - 1>();
       __syncwarp();
-      const uint32_t vat = at + kTileKeys * kpitch;
-      char* gat = mine + stage * stage_bytes + kTileKeys * kpitch + R::kV;
+      const uint32_t vat = at + kTileKeys * kpitch, gat = vat + R::kV;
       if constexpr (SCALAR) {
         // the decay of key (lane & 15), exp of the gates after it, goes to P
-        float x = reinterpret_cast<const float*>(gat)[lane & 15] * kLog2e;
+        float x;
+        lds_n<1>(gat + (lane & 15) * 4, &x);
+        x *= kLog2e;
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) {
           const float z = __shfl_down_sync(0xffffffffu, x, o, 16);
@@ -571,7 +597,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
         for (int x = 0; x < MT; ++x) {
           uint32_t va[4];
-          ldsm4t(vat + vaddr + (((x * 2 + vchunk) ^ r8) << 4), va);
+          ldsm4t(chunk_at(vat + vaddr, 2 * x), va);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -582,19 +608,17 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
         // gates -> decays in place, a lane on its channels from the newest key
         // back
         if (DV >= 32 || lane < DV) {
-          char* gl = gat + (VPL == 4 ? 0 : (lane * VPL % 4) * 4);
-          const int gch = lane * VPL / 4;
 #pragma unroll
           for (int key = kTileKeys - 1; key >= 0; --key) {
-            float* gp = reinterpret_cast<float*>(gl + key * R::kGPitch + ((gch ^ (key & 7)) << 4));
+            const uint32_t gp = chunk_at(gat + gmine, key & 7) + key * R::kGPitch;
             float x[VPL], d[VPL];
-            load_n<VPL>(gp, x);
+            lds_n<VPL>(gp, x);
 #pragma unroll
             for (int e = 0; e < VPL; ++e) {
               d[e] = ex2(suf[e]);
               suf[e] = fmaf(x[e], kLog2e, suf[e]);
             }
-            store_n<VPL>(gp, d);
+            sts_n<VPL>(gp, d);
           }
         }
         // P^T: the exact fp32 values, transposed as two 16-bit halves
@@ -614,19 +638,18 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
         for (int x = 0; x < MT; ++x) {
           uint32_t va[4];
-          ldsm4t(vat + vaddr + (((x * 2 + vchunk) ^ r8) << 4), va);
+          ldsm4t(chunk_at(vat + vaddr, 2 * x), va);
           uint32_t vh[8], vl[8];            // [2 key + channel half]
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) {
-            const char* gp = gat + 2 * j * R::kGPitch + ((lane >> 2) & 3) * 4;
-            const int c = x * 4 + (lane >> 4) + 2 * ch;
+            const uint32_t g0 = chunk_at(gat + gpair0, 4 * x + 2 * ch);
+            const uint32_t g1 = chunk_at(gat + gpair1, 4 * x + 2 * ch);
             const float2 v01 = unpack2(va[ch]), v23 = unpack2(va[2 + ch]);
-            const float d0 = *reinterpret_cast<const float*>(gp + ((c ^ (2 * j)) << 4));
-            const float d1 =
-                *reinterpret_cast<const float*>(gp + R::kGPitch + ((c ^ (2 * j + 1)) << 4));
-            const float d2 = *reinterpret_cast<const float*>(gp + 8 * R::kGPitch + ((c ^ (2 * j)) << 4));
-            const float d3 =
-                *reinterpret_cast<const float*>(gp + 9 * R::kGPitch + ((c ^ (2 * j + 1)) << 4));
+            float d0, d1, d2, d3;
+            lds_n<1>(g0, &d0);
+            lds_n<1>(g1, &d1);
+            lds_n<1>(g0 + 8 * R::kGPitch, &d2);
+            lds_n<1>(g1 + 8 * R::kGPitch, &d3);
             split_tf32(v01.x * d0, vh[ch], vl[ch]);
             split_tf32(v01.y * d1, vh[2 + ch], vl[2 + ch]);
             split_tf32(v23.x * d2, vh[4 + ch], vl[4 + ch]);
@@ -902,9 +925,9 @@ static fix_status paged_dims(const fix_attn_problem* p, const fix_attn_page_cach
   return line < INT32_MAX ? FIX_OK : FIX_ERR_SHAPE;
 }
 
-template <int DV, int NT, bool SCALAR>
+template <int DV, int NT, bool SCALAR, bool SAME>
 static fix_status paged_launch(const PagedArgs& a, const PagedPlan& pl, cudaStream_t st) {
-  auto* kernel = paged_decode_kernel<DV, NT, SCALAR>;
+  auto* kernel = paged_decode_kernel<DV, NT, SCALAR, SAME>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), pl.smem)) return FIX_ERR_CUDA;
   FIX_PAGED_TRY(OverlappedLaunch(dim3(pl.ctas), kPagedWarps * 32, pl.smem, st).run(kernel, a));
   const OverlappedLaunch join(dim3(pl.jobs, (a.hpb + a.heads_per_cta - 1) / a.heads_per_cta),
@@ -912,12 +935,14 @@ static fix_status paged_launch(const PagedArgs& a, const PagedPlan& pl, cudaStre
   return join.run(paged_join_kernel<DV>, a);
 }
 
-template <int DV>
-static fix_status paged_launch_dv(const PagedArgs& a, const PagedPlan& pl, bool scalar,
-                                  cudaStream_t st) {
-  if (scalar)
-    return pl.nt == 1 ? paged_launch<DV, 1, true>(a, pl, st) : paged_launch<DV, 2, true>(a, pl, st);
-  return pl.nt == 1 ? paged_launch<DV, 1, false>(a, pl, st) : paged_launch<DV, 2, false>(a, pl, st);
+template <int DV, bool SCALAR>
+static fix_status paged_launch_dv(const PagedArgs& a, const PagedPlan& pl, cudaStream_t st) {
+  const bool same = a.Dk == DV;
+  if (pl.nt == 1)
+    return same ? paged_launch<DV, 1, SCALAR, true>(a, pl, st)
+                : paged_launch<DV, 1, SCALAR, false>(a, pl, st);
+  return same ? paged_launch<DV, 2, SCALAR, true>(a, pl, st)
+              : paged_launch<DV, 2, SCALAR, false>(a, pl, st);
 }
 
 }  // namespace fix
@@ -978,9 +1003,9 @@ extern "C" fix_status fix_attn_decode_paged(const fix_attn_problem* p, const fix
   while (a.heads_per_cta * a.warps_per_head < 4 && a.heads_per_cta < pl.hpb) a.heads_per_cta *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (d.Dv) {
-    case 16: return paged_launch_dv<16>(a, pl, d.scalar_gate, st);
-    case 32: return paged_launch_dv<32>(a, pl, d.scalar_gate, st);
-    case 64: return paged_launch_dv<64>(a, pl, d.scalar_gate, st);
-    default: return paged_launch_dv<128>(a, pl, d.scalar_gate, st);
+    case 16: return d.scalar_gate ? paged_launch_dv<16, true>(a, pl, st) : paged_launch_dv<16, false>(a, pl, st);
+    case 32: return d.scalar_gate ? paged_launch_dv<32, true>(a, pl, st) : paged_launch_dv<32, false>(a, pl, st);
+    case 64: return d.scalar_gate ? paged_launch_dv<64, true>(a, pl, st) : paged_launch_dv<64, false>(a, pl, st);
+    default: return d.scalar_gate ? paged_launch_dv<128, true>(a, pl, st) : paged_launch_dv<128, false>(a, pl, st);
   }
 }
