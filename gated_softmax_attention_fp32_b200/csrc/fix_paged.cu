@@ -5,10 +5,16 @@
 // followed by the norm (or division by l = sum_s exp(S_s - m)) and the output
 // gate.
 //
+// Measured (B200, copy rate 6568 GB/s), Hq 32, Hkv 8, D 128, element-wise
+// gate: one sequence of 131,071 tokens in 174 us, 6.2 TB/s; 64 of 1 to 8,191
+// in 107 us, 5.7 TB/s; one of 257 in 10.4 us.
+//
 // What bounds it: every cached byte is read once (1 KB per key and kv head at
-// D 128 with the element-wise gate), against 2 flops per q head and channel
-// and one exponential per channel, so it should run at memory speed as long
-// as a key costs each SM fewer than about 40 cycles.
+// D 128 with the element-wise gate), against 4 flops per q head and channel
+// and one exponential per channel, so it runs at memory speed as long as a
+// key costs each SM fewer than about 40 cycles.  Around that a call pays some
+// 10 us: two launches, the dependent reads lengths -> page table -> tile, and
+// the join.
 //
 // Work split (paged_decode_kernel).  A unit is one (sequence, kv head, block
 // of up to 8 NT q heads of its group); its keys are cut into tiles of 16.

@@ -13,6 +13,10 @@
 // token's position, then the sines and cosines (two angles per lane, shared
 // within the warp; a lane's units all have the same pairs, as the units of a
 // head divide 32), then rotates and stores.
+//
+// Measured (B200, copy rate 6568 GB/s): 16,384 tokens of 16 + 4 heads of 128
+// in 29.7 us, 5.65 TB/s; 4,859 prompt tokens of 16 + 4 heads into pages of 16
+// in 18.3 us, 4.6 TB/s; one token of 32 + 8 heads in 2.9 us.
 #include "fix_internal.h"
 
 #define FIX_ROT_TRY(expr)             \
