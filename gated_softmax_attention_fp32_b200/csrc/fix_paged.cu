@@ -265,30 +265,38 @@ struct Ring {
   }
 };
 
-// The N channels of one lane of a finished row: y = o f [w] [swish(z)].
+// The N channels of one lane of a finished row, y = o f [w] [swish(z)]; w and z
+// are read when the object is made.
 template <int N>
-__device__ __forceinline__ void store_row(const PagedArgs& a, size_t row0, int c0, const float* o,
-                                          float f, bool none) {
-  float y[N];
+struct Finish {
+  float by[N];
+  __device__ __forceinline__ Finish(const PagedArgs& a, size_t row0, int c0, bool read) {
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    y[e] = o[e] * f;
-    if (!a.no_norm) y[e] *= bf2f(a.w[c0 + e]);
-    if (none) y[e] = 0.f;
-    if (a.z) y[e] *= swish(bf2f(a.z[row0 + c0 + e]));
+    for (int e = 0; e < N; ++e) {
+      by[e] = 1.f;
+      if (read && !a.no_norm) by[e] = bf2f(a.w[c0 + e]);
+      if (read && a.z) by[e] *= swish(bf2f(a.z[row0 + c0 + e]));
+    }
   }
-  if (a.y_f32) {
-    float* d = reinterpret_cast<float*>(a.y) + row0 + c0;
-    if constexpr (N == 4) *reinterpret_cast<float4*>(d) = make_float4(y[0], y[1], y[2], y[3]);
-    else if constexpr (N == 2) *reinterpret_cast<float2*>(d) = make_float2(y[0], y[1]);
-    else *d = y[0];
-  } else {
-    __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(a.y) + row0 + c0;
-    if constexpr (N == 4) *reinterpret_cast<uint2*>(d) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
-    else if constexpr (N == 2) *reinterpret_cast<uint32_t*>(d) = pack2(y[0], y[1]);
-    else *d = f2bf(y[0]);
+  __device__ __forceinline__ void store(const PagedArgs& a, size_t row0, int c0, const float* o,
+                                        float f, bool none) const {
+    float y[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) y[e] = none ? 0.f : o[e] * f * by[e];
+    if (a.y_f32) {
+      float* d = reinterpret_cast<float*>(a.y) + row0 + c0;
+      if constexpr (N == 4) *reinterpret_cast<float4*>(d) = make_float4(y[0], y[1], y[2], y[3]);
+      else if constexpr (N == 2) *reinterpret_cast<float2*>(d) = make_float2(y[0], y[1]);
+      else *d = y[0];
+    } else {
+      __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(a.y) + row0 + c0;
+      if constexpr (N == 4)
+        *reinterpret_cast<uint2*>(d) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+      else if constexpr (N == 2) *reinterpret_cast<uint32_t*>(d) = pack2(y[0], y[1]);
+      else *d = f2bf(y[0]);
+    }
   }
-}
+};
 template <int N>
 __device__ __forceinline__ void load_n(const float* p, float* x) {
   if constexpr (N == 4) {
@@ -716,7 +724,8 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
         if (in_row) load_n<VPL>(so + h * OP + c0, o);
         const float lh = sml[2 * h + 1];
         const float f = row_factor<VPL>(a, o, lh, DV);
-        if (in_row) store_row<VPL>(a, ((size_t)b * a.Hq + h0 + h) * DV, c0, o, f, lh == 0.f);
+        const size_t row0 = ((size_t)b * a.Hq + h0 + h) * DV;
+        if (in_row) Finish<VPL>(a, row0, c0, true).store(a, row0, c0, o, f, lh == 0.f);
       }
       if (a.join_by_unit && lane == 0) a.jobs[b * upb + u] = make_int4(0, 0, 0, 0);
     } else {
@@ -782,7 +791,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 job = a.jobs[blockIdx.x];
   const int np = job.x;
-  if (np < 2) return;
+  // (the bounds hold unless the workspace or the lengths were written meanwhile)
+  if (np < 2 || job.y < 0 || np > a.nworkers - job.y || (unsigned)job.z >= (unsigned)(a.B * upb))
+    return;
   const int b = job.z / upb, u = job.z % upb;
   const int kv = u / a.nhb, hb = u % a.nhb;
   const int nh = min(a.hpb, a.grp - hb * a.hpb);
@@ -791,7 +802,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   if (blockIdx.y * a.heads_per_cta >= nh) return;
   const int c0 = lane * VPL;
   const bool live = h < nh && c0 < DV;
-  const int i0 = (int)((long long)np * run / wph), i1 = (int)((long long)np * (run + 1) / wph);
+  const size_t row0 = ((size_t)b * a.Hq + kv * a.grp + hb * a.hpb + h) * DV;
+  const Finish<VPL> finish(a, row0, c0, live && run == 0);
+  const int runs = min(wph, (np + kDeep - 1) / kDeep);      // warps that have pieces
+  const int i0 = run < runs ? np * run / runs : 0, i1 = run < runs ? np * (run + 1) / runs : 0;
   const int tail = a.hpb * DV;
   float M = -INFINITY, l = 0.f, o[VPL], after[VPL];
 #pragma unroll
@@ -845,13 +859,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   if (run != 0 || h >= nh) return;
   // this head's runs, newest first
   M = -INFINITY;
-  for (int i = 0; i < wph; ++i) M = fmaxf(M, sml[warp + i][0]);
+  for (int i = 0; i < runs; ++i) M = fmaxf(M, sml[warp + i][0]);
   if (M == -INFINITY) M = 0.f;
   l = 0.f;
 #pragma unroll
   for (int e = 0; e < VPL; ++e) o[e] = after[e] = 0.f;
 #pragma unroll 4
-  for (int i = wph - 1; i >= 0; --i) {
+  for (int i = runs - 1; i >= 0; --i) {
     const float f = ex2(sml[warp + i][0] - M), li = sml[warp + i][1];
     l += f * li;
     if (!live) continue;
@@ -862,8 +876,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     }
   }
   const float f = row_factor<VPL>(a, o, l, DV);
-  if (live)
-    store_row<VPL>(a, ((size_t)b * a.Hq + kv * a.grp + hb * a.hpb + h) * DV, c0, o, f, l == 0.f);
+  if (live) finish.store(a, row0, c0, o, f, l == 0.f);
 }
 
 // ---------------------------------------------------------------- host side
