@@ -73,7 +73,7 @@ struct PagedArgs {
   long long slot_floats;               // floats per slot: hpb (DV + 2) + DV
   float* slots;                        // two per worker
   int4* jobs;                          // the join's work: (pieces, first worker, unit)
-  int join_by_unit, heads_per_cta, warps_per_head;   // shape of the join
+  int join_by_unit, heads_per_cta, warps_per_head, heads_per_warp;   // shape of the join
 };
 
 __device__ __forceinline__ int paged_len(const PagedArgs& a, int b) {
@@ -776,16 +776,18 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 
 // Joins the pieces of the units that were cut.  grid.x: the units, or (where
 // there are more units than workers) the workers, each for the cut unit that
-// begins in its span; grid.y: the head blocks' heads, heads_per_cta at a time.
-// A head has warps_per_head warps, each for a run of its pieces, newest first
-// and kDeep pieces at a time (what it costs is the latency of its loads);
-// channels lie over the lanes.
-template <int DV>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+// begins in its span; grid.y: the head block's heads, heads_per_cta at a time.
+// What it costs is the latency of its loads and, with many rows, their number:
+//   HPW = 1: a head has warps_per_head warps, each for a run of its pieces,
+//     four pieces at a time;
+//   HPW = 4: a warp has four heads, which share the reads of the pieces' gate
+//     totals, two pieces at a time.
+// Pieces are taken newest first; channels lie over the lanes.
+template <int DV, int HPW>
+__global__ void __launch_bounds__(kJoinWarps * 32 / HPW)
     paged_join_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int VPL = DV >= 32 ? DV / 32 : 1;
-  constexpr int kDeep = 4;      // 8 is no faster, and slower for few pieces
-  __shared__ float so[kJoinWarps][DV], stot[kJoinWarps][DV], sml[kJoinWarps][2];
+  constexpr int kDeep = HPW == 1 ? 4 : 2;      // 8 is no faster, and slower for few pieces
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int upb = a.Hkv * a.nhb;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -797,86 +799,121 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int b = job.z / upb, u = job.z % upb;
   const int kv = u / a.nhb, hb = u % a.nhb;
   const int nh = min(a.hpb, a.grp - hb * a.hpb);
-  const int wph = a.warps_per_head;
-  const int h = blockIdx.y * a.heads_per_cta + warp / wph, run = warp % wph;
+  const int wph = HPW == 1 ? a.warps_per_head : 1;
+  const int h = blockIdx.y * a.heads_per_cta + warp / wph * HPW, run = warp % wph;   // and HPW - 1 more
   if (blockIdx.y * a.heads_per_cta >= nh) return;
   const int c0 = lane * VPL;
   const bool live = h < nh && c0 < DV;
   const size_t row0 = ((size_t)b * a.Hq + kv * a.grp + hb * a.hpb + h) * DV;
-  const Finish<VPL> finish(a, row0, c0, live && run == 0);
+  const Finish<VPL> finish(a, row0, c0, live && run == 0 && HPW == 1);
   const int runs = min(wph, (np + kDeep - 1) / kDeep);      // warps that have pieces
   const int i0 = run < runs ? np * run / runs : 0, i1 = run < runs ? np * (run + 1) / runs : 0;
   const int tail = a.hpb * DV;
-  float M = -INFINITY, l = 0.f, o[VPL], after[VPL];
+  float M[HPW], l[HPW], o[HPW][VPL], after[VPL];
 #pragma unroll
-  for (int e = 0; e < VPL; ++e) o[e] = after[e] = 0.f;
+  for (int k = 0; k < HPW; ++k) {
+    M[k] = -INFINITY;
+    l[k] = 0.f;
+#pragma unroll
+    for (int e = 0; e < VPL; ++e) o[k][e] = 0.f;
+  }
+#pragma unroll
+  for (int e = 0; e < VPL; ++e) after[e] = 0.f;
   if (live) {
     for (int i = i1 - 1; i >= i0; i -= kDeep) {
-      float pm[kDeep], pl[kDeep], x[kDeep][VPL], t[kDeep][VPL];
+      float pm[kDeep][HPW], pl[kDeep][HPW], x[kDeep][HPW][VPL], t[kDeep][VPL];
 #pragma unroll
       for (int d = 0; d < kDeep; ++d) {
         // a run's last batch may be short: its missing pieces count nothing
         const bool there = i - d >= i0;
         const float* s = a.slots + (2LL * (job.y + i - d) + (i == d)) * a.slot_floats;
-        pm[d] = there ? s[tail + DV + 2 * h] : -INFINITY;
-        pl[d] = there ? s[tail + DV + 2 * h + 1] : 0.f;
 #pragma unroll
-        for (int e = 0; e < VPL; ++e) x[d][e] = t[d][e] = 0.f;
-        if (there) {
-          load_n<VPL>(s + h * DV + c0, x[d]);
-          load_n<VPL>(s + tail + c0, t[d]);
+        for (int k = 0; k < HPW; ++k) {
+          const bool head = there && h + k < nh;
+          pm[d][k] = head ? s[tail + DV + 2 * (h + k)] : -INFINITY;
+          pl[d][k] = head ? s[tail + DV + 2 * (h + k) + 1] : 0.f;
+#pragma unroll
+          for (int e = 0; e < VPL; ++e) x[d][k][e] = 0.f;
+          if (head) load_n<VPL>(s + (h + k) * DV + c0, x[d][k]);
         }
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) t[d][e] = 0.f;
+        if (there) load_n<VPL>(s + tail + c0, t[d]);
       }
-      float mx = M;
+      float ref[HPW];
 #pragma unroll
-      for (int d = 0; d < kDeep; ++d) mx = fmaxf(mx, pm[d]);
-      const float ref = mx == -INFINITY ? 0.f : mx, f0 = ex2(M - ref);
-      M = mx;
-      l *= f0;
+      for (int k = 0; k < HPW; ++k) {
+        float mx = M[k];
 #pragma unroll
-      for (int e = 0; e < VPL; ++e) o[e] *= f0;
+        for (int d = 0; d < kDeep; ++d) mx = fmaxf(mx, pm[d][k]);
+        ref[k] = mx == -INFINITY ? 0.f : mx;
+        const float f0 = ex2(M[k] - ref[k]);
+        M[k] = mx;
+        l[k] *= f0;
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) o[k][e] *= f0;
+      }
 #pragma unroll
       for (int d = 0; d < kDeep; ++d) {
-        // a piece without weight adds nothing, whatever the gates: those of the
-        // sequence's first token, which no decay uses, are in `after` by then
-        const float f = ex2(pm[d] - ref);
-        l += f * pl[d];
+        float decay[VPL];
 #pragma unroll
         for (int e = 0; e < VPL; ++e) {
-          if (pl[d] != 0.f) o[e] += f * x[d][e] * ex2(after[e]);
+          decay[e] = ex2(after[e]);
           after[e] += t[d][e];
+        }
+#pragma unroll
+        for (int k = 0; k < HPW; ++k) {
+          // a piece without weight adds nothing, whatever the gates: that of the
+          // sequence's first token, which no decay uses, is in `after` by then
+          const float f = ex2(pm[d][k] - ref[k]);
+          l[k] += f * pl[d][k];
+#pragma unroll
+          for (int e = 0; e < VPL; ++e)
+            if (pl[d][k] != 0.f) o[k][e] += f * x[d][k][e] * decay[e];
         }
       }
     }
-    store_n<VPL>(&so[warp][c0], o);
-    store_n<VPL>(&stot[warp][c0], after);
-    if (lane == 0) {
-      sml[warp][0] = M;
-      sml[warp][1] = l;
-    }
   }
-  __syncthreads();
-  if (run != 0 || h >= nh) return;
-  // this head's runs, newest first
-  M = -INFINITY;
-  for (int i = 0; i < runs; ++i) M = fmaxf(M, sml[warp + i][0]);
-  if (M == -INFINITY) M = 0.f;
-  l = 0.f;
+  if constexpr (HPW > 1) {
 #pragma unroll
-  for (int e = 0; e < VPL; ++e) o[e] = after[e] = 0.f;
+    for (int k = 0; k < HPW; ++k) {
+      if (h + k >= nh) break;
+      const size_t row = row0 + k * DV;
+      const float f = row_factor<VPL>(a, o[k], l[k], DV);
+      if (live) Finish<VPL>(a, row, c0, true).store(a, row, c0, o[k], f, l[k] == 0.f);
+    }
+  } else {
+    __shared__ float so[kJoinWarps][DV], stot[kJoinWarps][DV], sml[kJoinWarps][2];
+    if (live) {
+      store_n<VPL>(&so[warp][c0], o[0]);
+      store_n<VPL>(&stot[warp][c0], after);
+      if (lane == 0) {
+        sml[warp][0] = M[0];
+        sml[warp][1] = l[0];
+      }
+    }
+    __syncthreads();
+    if (run != 0 || h >= nh) return;
+    // this head's runs, newest first
+    float top = -INFINITY, sum = 0.f, y[VPL];
+    for (int i = 0; i < runs; ++i) top = fmaxf(top, sml[warp + i][0]);
+    if (top == -INFINITY) top = 0.f;
+#pragma unroll
+    for (int e = 0; e < VPL; ++e) y[e] = after[e] = 0.f;
 #pragma unroll 4
-  for (int i = runs - 1; i >= 0; --i) {
-    const float f = ex2(sml[warp + i][0] - M), li = sml[warp + i][1];
-    l += f * li;
-    if (!live) continue;
+    for (int i = runs - 1; i >= 0; --i) {
+      const float f = ex2(sml[warp + i][0] - top), li = sml[warp + i][1];
+      sum += f * li;
+      if (!live) continue;
 #pragma unroll
-    for (int e = 0; e < VPL; ++e) {
-      if (li != 0.f) o[e] += f * so[warp + i][c0 + e] * ex2(after[e]);
-      after[e] += stot[warp + i][c0 + e];
+      for (int e = 0; e < VPL; ++e) {
+        if (li != 0.f) y[e] += f * so[warp + i][c0 + e] * ex2(after[e]);
+        after[e] += stot[warp + i][c0 + e];
+      }
     }
+    const float f = row_factor<VPL>(a, y, sum, DV);
+    if (live) finish.store(a, row0, c0, y, f, sum == 0.f);
   }
-  const float f = row_factor<VPL>(a, o, l, DV);
-  if (live) finish.store(a, row0, c0, o, f, l == 0.f);
 }
 
 // ---------------------------------------------------------------- host side
@@ -950,8 +987,9 @@ static fix_status paged_launch(const PagedArgs& a, const PagedPlan& pl, cudaStre
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), pl.smem)) return FIX_ERR_CUDA;
   FIX_PAGED_TRY(OverlappedLaunch(dim3(pl.ctas), kPagedWarps * 32, pl.smem, st).run(kernel, a));
   const OverlappedLaunch join(dim3(pl.jobs, (a.hpb + a.heads_per_cta - 1) / a.heads_per_cta),
-                              a.heads_per_cta * a.warps_per_head * 32, 0, st);
-  return join.run(paged_join_kernel<DV>, a);
+                              a.heads_per_cta / a.heads_per_warp * a.warps_per_head * 32, 0, st);
+  return a.heads_per_warp == 4 ? join.run(paged_join_kernel<DV, 4>, a)
+                               : join.run(paged_join_kernel<DV, 1>, a);
 }
 
 template <int DV, bool SCALAR>
@@ -1010,7 +1048,9 @@ extern "C" fix_status fix_attn_decode_paged(const fix_attn_problem* p, const fix
   a.jobs = static_cast<int4*>(workspace);
   a.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.job_bytes);
   // warps per head: about one per piece that a unit of average length has, up
-  // to some 4096 in all (28 per SM); CTAs of four warps at least
+  // to some 4096 in all (28 per SM), and four heads per warp where the rows are
+  // more (256 sequences, 2 kv heads, 16 q heads each: 52.9 -> 51.7 us); CTAs of four
+  // warps where there are heads enough
   a.join_by_unit = pl.units <= pl.workers;
   const int pieces = pl.workers / pl.jobs;
   const long long rows = (long long)pl.jobs * pl.hpb;
@@ -1018,8 +1058,9 @@ extern "C" fix_status fix_attn_decode_paged(const fix_attn_problem* p, const fix
   while (a.warps_per_head < kJoinWarps && 2 * a.warps_per_head <= pieces &&
          rows * 2 * a.warps_per_head <= 4096)
     a.warps_per_head *= 2;
-  a.heads_per_cta = 1;
-  while (a.heads_per_cta * a.warps_per_head < 4 && a.heads_per_cta < pl.hpb) a.heads_per_cta *= 2;
+  a.heads_per_cta = a.heads_per_warp = rows > 4096 && pl.hpb >= 4 ? 4 : 1;
+  while (a.heads_per_cta / a.heads_per_warp * a.warps_per_head < 4 && a.heads_per_cta < pl.hpb)
+    a.heads_per_cta *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (d.Dv) {
     case 16: return d.scalar_gate ? paged_launch_dv<16, true>(a, pl, st) : paged_launch_dv<16, false>(a, pl, st);

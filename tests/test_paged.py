@@ -968,3 +968,19 @@ def test_integer_arrays_at_any_offset_and_the_unused_first_gate(cuda_lib):
     pos = [lens[0] - 1, lens[2] - 2, lens[2] - 1]
     got = torch.stack([kp[int(table[b, p // 16]), p % 16] for b, p in zip((0, 2, 2), pos)])
     check_rotated(got, x.cpu(), pos, inv_freq(64))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,hi,scalar", [(300, 32, 2, 300, False), (300, 20, 2, 300, True),
+                                                (600, 20, 4, 80, False)])
+def test_decode_paged_many_rows_to_join(cuda_lib, B, Hq, Hkv, hi, scalar):
+    """Thousands of (sequence, q head) rows whose pieces are joined, with fewer
+    and with more units than the split has workers."""
+    gen = torch.Generator().manual_seed(B + Hq)
+    lens = torch.randint(0, hi, (B,), generator=gen).tolist()
+    c = Cache(lens, Hkv, 32, 32, 16, seed=15, scalar=scalar)
+    q, w, z = decode_inputs(B, Hq, 32, 32, 16, True)
+    for norm in (True, False):
+        y = fixattn.fix_attn_decode_paged(q.cuda(), *c.cuda(), w.cuda(), y_dtype=torch.float32, o_gate=z.cuda(),
+                                          o_norm=norm)
+        check_decode(y, c, q, w, z, norm=norm, rows=list(range(0, B, 23)) + [B - 1])
