@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
         *a.status = FIX_ERR_PAGE;
       continue;
     }
-    for (int e = threadIdx.x; e < a.Hq * DV; e += blockDim.x) {
+    for (long long e = threadIdx.x; e < (long long)a.Hq * DV; e += blockDim.x) {
       const size_t at = (size_t)b * a.Hq * DV + e;
       if (a.y_f32) reinterpret_cast<float*>(a.y)[at] = 0.f;
       else reinterpret_cast<__nv_bfloat16*>(a.y)[at] = f2bf(0.f);

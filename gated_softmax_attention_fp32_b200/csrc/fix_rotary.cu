@@ -240,6 +240,8 @@ static fix_status token_dims(const fix_attn_problem* p, Dims* d) {
   dense.cu_seqlens_host = nullptr;
   dense.num_seqs = 0;
   FIX_ROT_TRY(validate_problem(&dense, d));
+  // a token's runs of units fit a grid's y (below 65,536)
+  if ((long long)d->Hq * (d->Dk > d->Dv ? d->Dk : d->Dv) > (1 << 25)) return FIX_ERR_SHAPE;
   if (!p->cu_seqlens) return p->num_seqs || p->cu_seqlens_host ? FIX_ERR_CU_SEQLENS : FIX_OK;
   if (p->batch != 1) return FIX_ERR_SHAPE;
   if (p->num_seqs < 1) return FIX_ERR_CU_SEQLENS;
@@ -275,8 +277,7 @@ static fix_status launch_tokens(TokenArgs& a, cudaStream_t st) {
   const long long per_lane = units > 32 ? (units + 31) / 32 : 1;
   int most = 8;
   while (most > 1 && (long long)a.N * ((per_lane + most - 1) / most) < 148 * 8) most /= 2;
-  long long runs = (per_lane + most - 1) / most;
-  if (runs > 65535) return FIX_ERR_SHAPE;
+  const long long runs = (per_lane + most - 1) / most;
   a.items = (int)((per_lane + runs - 1) / runs);
   const OverlappedLaunch launch(dim3((a.N + kTokWarps - 1) / kTokWarps, (unsigned)runs),
                                 kTokWarps * 32, 0, st);

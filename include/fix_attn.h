@@ -224,7 +224,8 @@ typedef struct {
  * Packed: problem.cu_seqlens (device) is read, cu_seqlens_host may be NULL
  * (nothing is planned on the host); tokens behind the last sequence are
  * copied without a rotation.
- * `inverse` != 0 turns by -t: the gradient, and the inverse. */
+ * `inverse` != 0 turns by -t: the gradient, and the inverse.
+ * Here and in the append, Hq times the larger head dim is at most 2^25. */
 fix_status fix_attn_rotary(const fix_attn_problem *p, const fix_attn_rotation *r,
                            const int32_t *positions, const void *q, int64_t q_stride,
                            const void *k, int64_t k_stride, void *q_out, void *k_out,

@@ -174,6 +174,7 @@ NULL, SHAPE, HEAD, GQA, CU, ALIGN, WS = 1, 2, 3, 4, 5, 6, 7
     (dict(num_q_heads=3), {}, {}, GQA),
     (dict(batch=0), {}, {}, SHAPE),
     (dict(num_seqs=2), {}, {}, CU),
+    (dict(num_q_heads=1 << 21), {}, {}, SHAPE),
     (dict(cu_seqlens=A, num_seqs=2), {}, {}, SHAPE),          # packed wants batch 1
     (dict(cu_seqlens=A, batch=1), {}, {}, CU),                # no sequence count
     (dict(cu_seqlens=A + 4, batch=1, num_seqs=2), {}, {}, ALIGN),
