@@ -294,8 +294,8 @@ fix_status fix_attn_append_paged(const fix_attn_problem *p, const fix_attn_page_
  * a sequence's length are never read.  g should be <= 0; positive gates are
  * computed the same way while exp of their sum over any run of tokens stays
  * inside the float32 range.  Any Hq/Hkv; with C = max_pages * page_size (or 2^31 - 1 if less)
- * and r = ceil(Hq/Hkv / 16), B * Hkv * r * (C / 16 + 4) must stay below 2^31
- * (FIX_ERR_SHAPE).  The work is split over the cache on the device by
+ * and r = ceil(Hq/Hkv / 16), B * Hkv * r * (C / 16 + 4) must stay below 2^31 -
+ * 2^16 (FIX_ERR_SHAPE).  The work is split over the cache on the device by
  * the lengths found there, so a captured call may be replayed with others.
  * The workspace needs no initialisation; calls that may overlap need one
  * each. */
