@@ -6,8 +6,8 @@
 // gate.
 //
 // Measured (B200, copy rate 6568 GB/s), Hq 32, Hkv 8, D 128, element-wise
-// gate: one sequence of 131,071 tokens in 174 us, 6.2 TB/s; 64 of 1 to 8,191
-// in 107 us, 5.7 TB/s; one of 257 in 10.4 us.
+// gate: one sequence of 131,071 tokens in 170 to 174 us, 6.2 TB/s; 64 of 1 to
+// 8,191 in 103 to 106 us, 5.8 TB/s; one of 257 in 9.5 us.
 //
 // What bounds it: every cached byte is read once (1 KB per key and kv head at
 // D 128 with the element-wise gate), against 4 flops per q head and channel

@@ -15,8 +15,8 @@
 // head divide 32), then rotates and stores.
 //
 // Measured (B200, copy rate 6568 GB/s): 16,384 tokens of 16 + 4 heads of 128
-// in 29.7 us, 5.65 TB/s; 4,859 prompt tokens of 16 + 4 heads into pages of 16
-// in 18.3 us, 4.6 TB/s; one token of 32 + 8 heads in 2.9 us.
+// in 29.0 us, 5.8 TB/s; 4,859 prompt tokens of 16 + 4 heads into pages of 16
+// in 18.4 us, 4.6 TB/s; one token of 32 + 8 heads in 2.8 us.
 #include "fix_internal.h"
 
 #define FIX_ROT_TRY(expr)             \

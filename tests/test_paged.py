@@ -931,13 +931,14 @@ def test_rotary_gradient_as_autograd_calls_it(cuda_lib):
         a, b = fixattn.fix_rotary(ql, kl, fd)
         return (a, b) + torch.autograd.grad((a, b), (ql, kl), (dq, dq))
 
+    torch.cuda.synchronize()
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
         step()
     torch.cuda.current_stream().wait_stream(s)
     graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
+    with torch.cuda.graph(graph, stream=s):
         out = step()
     with torch.no_grad():
         ql.copy_(mk(B, T, H, D))
