@@ -986,3 +986,52 @@ def test_decode_paged_many_rows_to_join(cuda_lib, B, Hq, Hkv, hi, scalar):
         y = fixattn.fix_attn_decode_paged(q.cuda(), *c.cuda(), w.cuda(), y_dtype=torch.float32, o_gate=z.cuda(),
                                           o_norm=norm)
         check_decode(y, c, q, w, z, norm=norm, rows=list(range(0, B, 23)) + [B - 1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("between", ["copy", "clear", "other stream", "nothing"])
+def test_captured_behind_copies_and_forks(cuda_lib, between):
+    """The calls' kernels are launched to overlap the end of the kernel before
+    them; in a graph they may follow a memory copy, a clear or a join of two
+    streams just as well, and see what those wrote."""
+    st = _step_state([30, 77], 81)
+    for x in st["pages"]:
+        x.copy_(torch.nan_to_num(x, nan=0.0))
+    src = {n: st[n].clone() for n in ("k", "seqlens")}
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        if between == "copy":
+            st["seqlens"].copy_(src["seqlens"])
+        elif between == "clear":
+            st["k"].zero_()
+        elif between == "other stream":
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                st["k"].copy_(src["k"])
+            torch.cuda.current_stream().wait_stream(side)
+        q, _ = fixattn.fix_attn_append_paged(st["k"], st["v"], st["g"], *st["pages"], st["table"], st["seqlens"],
+                                             q=st["q"], inv_freq=st["f"])
+        if between == "copy":
+            st["seqlens"].copy_(src["seqlens"])
+        elif between == "clear":
+            src["seqlens"].zero_()
+        return fixattn.fix_attn_decode_paged(q[:, 0], *st["pages"], st["table"], st["seqlens"], st["w"],
+                                             y_dtype=torch.float32)
+
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        want = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        y = step()
+    for _ in range(3):
+        y.fill_(NAN)
+        if between == "other stream":
+            st["k"].fill_(NAN)
+        if between == "copy":
+            st["seqlens"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
