@@ -703,15 +703,34 @@ def _aligned(t):
     return t.clone() if t.data_ptr() & 15 else t
 
 
+def _replan(saved, interleaved, sizes, rot_dim, index):
+    """A plan of the same sizes for what the saved tensors are by now: copies,
+    under saved-tensor hooks."""
+    inv_freq, cu_seqlens, positions = saved
+    if (inv_freq.dtype is not _f32 or inv_freq.get_device() != index or inv_freq.dim() != 1
+            or 2 * inv_freq.numel() != rot_dim or not inv_freq.is_contiguous()):
+        _dense("inv_freq", inv_freq, _f32, index, (rot_dim // 2,))
+    if sizes.num_seqs:
+        _dense("cu_seqlens", cu_seqlens, torch.int64, index, (sizes.num_seqs + 1,))
+        sizes = Problem.from_buffer_copy(sizes)
+        sizes.cu_seqlens = cu_seqlens.data_ptr()
+    if positions is not None:
+        _dense("positions", positions, _i32, index, (sizes.batch, sizes.seqlen))
+        positions = positions.data_ptr()
+    return sizes, Rotation(inv_freq.data_ptr(), rot_dim, 1 if interleaved else 0), positions
+
+
 class _FixRotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, inv_freq, cu_seqlens, positions, interleaved, inverse):
         index = _cuda_index("q", q)
         ctx.save_for_backward(inv_freq, cu_seqlens, positions)
-        ctx.cfg = (interleaved, inverse)
         with _elsewhere(index, None) or contextlib.nullcontext():
-            plan = ctx.plan = _rotary_plan(q, k, inv_freq, cu_seqlens, positions, interleaved,
-                                           index)
+            plan = _rotary_plan(q, k, inv_freq, cu_seqlens, positions, interleaved, index)
+            # of this plan the backward takes the sizes, not the addresses:
+            # under saved-tensor hooks (checkpoints, offload) the tensors may
+            # be gone by then
+            ctx.cfg = (interleaved, inverse, plan[0], plan[1].rot_dim)
             return _rotate(plan, q, _token_stride("q", q, q.shape[2] * q.shape[3]), k,
                            _token_stride("k", k, k.shape[2] * k.shape[3]), _dense_like(q),
                            _dense_like(k), inverse, index)
@@ -721,13 +740,14 @@ class _FixRotary(torch.autograd.Function):
         # the rotation is linear and orthogonal: its gradient is the rotation
         # back (itself differentiable)
         saved = ctx.saved_tensors            # raises where one was changed since
-        interleaved, inverse = ctx.cfg
+        interleaved, inverse, sizes, rot_dim = ctx.cfg
         dq, dk = _aligned(dq), _aligned(dk)
+        index = dq.get_device()
+        plan = _replan(saved, interleaved, sizes, rot_dim, index)
         if torch.is_grad_enabled():
             dq, dk = _FixRotary.apply(dq, dk, *saved, interleaved, not inverse)
         else:
-            dq, dk = _rotate(ctx.plan, dq, 0, dk, 0, _dense_like(dq), _dense_like(dk),
-                             not inverse, dq.get_device())
+            dq, dk = _rotate(plan, dq, 0, dk, 0, _dense_like(dq), _dense_like(dk), not inverse, index)
         return dq, dk, None, None, None, None, None
 
 
