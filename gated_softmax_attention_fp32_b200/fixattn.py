@@ -316,8 +316,10 @@ def fix_attn_decode(q, k_cache, v_cache, g_cache, seqlens, o_norm_weight=None, s
 # device index by identity and number, not torch.device objects).
 _Tensor = torch.Tensor
 _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (absent where torch was built without CUDA: the package imports there, and
+# every call refuses its tensors before it needs these)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _need(ok, what):
