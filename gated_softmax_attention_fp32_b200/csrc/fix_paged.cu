@@ -36,6 +36,10 @@
 // Element-wise gate: V' = D v and P are fp32 values, split into two tf32
 // parts each (11 bits and more), three products: about 2^-21.  Scalar gate:
 // V stays bf16, D goes to P, which is split into three bf16 parts (24 bits).
+// The tensor cores' own fp32 sums truncate, always towards zero, so that a sum
+// kept in them drifts (no gates, 32,768 keys in one warp: 2.8e-4 of y): they
+// add up one tile's products, from zero, and the running sums are added to
+// outside, rounding to nearest.
 // Gate sums are kept in units of log 2.
 #include <type_traits>
 
@@ -621,10 +625,14 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
           uint32_t va[4];
           ldsm4t(chunk_at(vat + vaddr, 2 * x), va);
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+          for (int t = 0; t < NT; ++t) {
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int part = 0; part < 3; ++part)
-              mma_bf16(acc[x][t], va, pb[t][part][0], pb[t][part][1]);
+            for (int part = 2; part >= 0; --part)
+              mma_bf16(sum, va, pb[t][part][0], pb[t][part][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[x][t][e] += sum[e];
+          }
         }
       } else {
         // gates -> decays in place, a lane on its channels from the newest key
@@ -678,13 +686,19 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
             split_tf32(v23.y * d3, vh[6 + ch], vl[6 + ch]);
           }
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+          for (int t = 0; t < NT; ++t) {
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-              mma_tf32(acc[x][t], vl + 4 * ks, ph[t][2 * ks], ph[t][2 * ks + 1]);
-              mma_tf32(acc[x][t], vh + 4 * ks, pl[t][2 * ks], pl[t][2 * ks + 1]);
-              mma_tf32(acc[x][t], vh + 4 * ks, ph[t][2 * ks], ph[t][2 * ks + 1]);
+              mma_tf32(sum, vl + 4 * ks, ph[t][2 * ks], ph[t][2 * ks + 1]);
+              mma_tf32(sum, vh + 4 * ks, pl[t][2 * ks], pl[t][2 * ks + 1]);
             }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+              mma_tf32(sum, vh + 4 * ks, ph[t][2 * ks], ph[t][2 * ks + 1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[x][t][e] += sum[e];
+          }
         }
       }
       __syncwarp();
