@@ -40,7 +40,11 @@
 // kept in them drifts (no gates, 32,768 keys in one warp: 2.8e-4 of y): they
 // add up one tile's products, from zero, and the running sums are added to
 // outside, rounding to nearest.
-// Gate sums are kept in units of log 2.
+// Gate sums are kept in units of log 2: a tile's gates are summed by
+// themselves, and the tile's sum is added to a compensated total (likewise
+// the pieces' totals in the join).  One running fp32 sum over all keys rounds
+// the same way at every step where the gates are steady (all of -1e-4, 32,768
+// keys in one warp: 9e-5 of y; now 1e-6).
 #include <type_traits>
 
 #include "fix_internal.h"
@@ -157,6 +161,45 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+
+// x += y and x += y c for N floats, two at a time where N is even.
+__device__ __forceinline__ void add_pair(float* x, const float* y) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n"
+      " add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
+      : "+f"(x[0]), "+f"(x[1])
+      : "f"(y[0]), "f"(y[1]));
+}
+__device__ __forceinline__ void fma_pair(float* x, const float* y, float c) {
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n"
+      " mov.b64 c, {%4, %4};\n fma.rn.f32x2 a, b, c, a;\n mov.b64 {%0, %1}, a;\n}"
+      : "+f"(x[0]), "+f"(x[1])
+      : "f"(y[0]), "f"(y[1]), "f"(c));
+}
+template <int N>
+__device__ __forceinline__ void add_n(float* x, const float* y) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) add_pair(x + e, y + e);
+  } else {
+    x[0] += y[0];
+  }
+}
+template <int N>
+__device__ __forceinline__ void fma_n(float* x, const float* y, float c) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) fma_pair(x + e, y + e, c);
+  } else {
+    x[0] = fmaf(y[0], c, x[0]);
+  }
+}
+// Adds x, which has the sum's `lost` in it already, and notes what that
+// rounds off (compensated summation); a sum that is not finite loses nothing.
+__device__ __forceinline__ void add_exactly(float& sum, float& lost, float x) {
+  const float s = sum + x;
+  lost = fabsf(s) < INFINITY ? x - (s - sum) : 0.f;
+  sum = s;
+}
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -497,7 +540,8 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
     }
 
     float acc[MT][NT][4];
-    float m[NT][2], l[NT][2], suf[VPL];
+    // of the gates after a tile: their sum and what its roundings lost
+    float m[NT][2], l[NT][2], suf[VPL], lost[VPL];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -512,7 +556,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
         l[t][e] = 0.f;
       }
 #pragma unroll
-    for (int e = 0; e < VPL; ++e) suf[e] = 0.f;
+    for (int e = 0; e < VPL; ++e) suf[e] = lost[e] = 0.f;
 
     for (int i = 0; i < n; ++i) {
       const int stage = ST == 1 ? 0 : (i & 1);
@@ -601,8 +645,8 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
         }
         float after = __shfl_down_sync(0xffffffffu, x, 1, 16);
         if ((lane & 15) == 15) after = 0.f;
-        const float d = ex2(suf[0] + after);
-        suf[0] += __shfl_sync(0xffffffffu, x, 0, 16);
+        const float d = ex2(suf[0] + (after + lost[0]));
+        add_exactly(suf[0], lost[0], __shfl_sync(0xffffffffu, x, 0, 16) + lost[0]);
         const float d0 = __shfl_sync(0xffffffffu, d, key0), d1 = __shfl_sync(0xffffffffu, d, key0 + 8);
         uint32_t pb[NT][3][2];
 #pragma unroll
@@ -630,26 +674,31 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
             for (int part = 2; part >= 0; --part)
               mma_bf16(sum, va, pb[t][part][0], pb[t][part][1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[x][t][e] += sum[e];
+            add_n<4>(acc[x][t], sum);
           }
         }
       } else {
         // gates -> decays in place, a lane on its channels from the newest key
         // back
         if (DV >= 32 || lane < DV) {
+          float own[VPL];                    // the tile's sum, with what the total has lost
+#pragma unroll
+          for (int e = 0; e < VPL; ++e) own[e] = lost[e];
 #pragma unroll
           for (int key = kTileKeys - 1; key >= 0; --key) {
             const uint32_t gp = chunk_at(gat + gmine, key & 7) + key * R::kGPitch;
             float x[VPL], d[VPL];
             lds_n<VPL>(gp, x);
 #pragma unroll
-            for (int e = 0; e < VPL; ++e) {
-              d[e] = ex2(suf[e]);
-              suf[e] = fmaf(x[e], kLog2e, suf[e]);
-            }
+            for (int e = 0; e < VPL; ++e) d[e] = suf[e];
+            add_n<VPL>(d, own);
+#pragma unroll
+            for (int e = 0; e < VPL; ++e) d[e] = ex2(d[e]);
+            fma_n<VPL>(own, x, kLog2e);
             sts_n<VPL>(gp, d);
           }
+#pragma unroll
+          for (int e = 0; e < VPL; ++e) add_exactly(suf[e], lost[e], own[e]);
         }
         // P^T: the exact fp32 values, transposed as two 16-bit halves
         uint32_t ph[NT][4], pl[NT][4];                       // keys 2j, 2j + 1, 2j + 8, 2j + 9
@@ -696,8 +745,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
               mma_tf32(sum, vh + 4 * ks, ph[t][2 * ks], ph[t][2 * ks + 1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[x][t][e] += sum[e];
+            add_n<4>(acc[x][t], sum);
           }
         }
       }
@@ -832,7 +880,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32 / HPW)
   const int runs = min(wph, (np + kDeep - 1) / kDeep);      // warps that have pieces
   const int i0 = run < runs ? np * run / runs : 0, i1 = run < runs ? np * (run + 1) / runs : 0;
   const int tail = a.hpb * DV;
-  float M[HPW], l[HPW], o[HPW][VPL], after[VPL];
+  float M[HPW], l[HPW], o[HPW][VPL], after[VPL], lost[VPL];
 #pragma unroll
   for (int k = 0; k < HPW; ++k) {
     M[k] = -INFINITY;
@@ -841,7 +889,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32 / HPW)
     for (int e = 0; e < VPL; ++e) o[k][e] = 0.f;
   }
 #pragma unroll
-  for (int e = 0; e < VPL; ++e) after[e] = 0.f;
+  for (int e = 0; e < VPL; ++e) after[e] = lost[e] = 0.f;
   if (live) {
     for (int i = i1 - 1; i >= i0; i -= kDeep) {
       float pm[kDeep][HPW], pl[kDeep][HPW], x[kDeep][HPW][VPL], t[kDeep][VPL];
@@ -876,13 +924,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32 / HPW)
 #pragma unroll
         for (int e = 0; e < VPL; ++e) o[k][e] *= f0;
       }
+      float own[VPL];                    // the batch's sum, with what the total has lost
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) own[e] = lost[e];
 #pragma unroll
       for (int d = 0; d < kDeep; ++d) {
         float decay[VPL];
 #pragma unroll
         for (int e = 0; e < VPL; ++e) {
-          decay[e] = ex2(after[e]);
-          after[e] += t[d][e];
+          decay[e] = ex2(after[e] + own[e]);
+          own[e] += t[d][e];
         }
 #pragma unroll
         for (int k = 0; k < HPW; ++k) {
@@ -895,6 +946,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32 / HPW)
             if (pl[d][k] != 0.f) o[k][e] += f * x[d][k][e] * decay[e];
         }
       }
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) add_exactly(after[e], lost[e], own[e]);
     }
   }
   if constexpr (HPW > 1) {
