@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 
     float acc[MT][NT][4];
     // of the gates after a tile: their sum and what its roundings lost
-    float m[NT][2], l[NT][2], suf[VPL], lost[VPL];
+    float m[NT][2], l[NT][2], llost[NT][2], suf[VPL], lost[VPL];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         m[t][e] = -INFINITY;
-        l[t][e] = 0.f;
+        l[t][e] = llost[t][e] = 0.f;
       }
 #pragma unroll
     for (int e = 0; e < VPL; ++e) suf[e] = lost[e] = 0.f;
@@ -618,7 +618,10 @@ __global__ void __launch_bounds__(kPagedWarps * 32, NT == 1 ? 3 : 2)
           m[t][e] = x;
           p[t][e] = ex2(s[t][e] - ref);
           p[t][2 + e] = ex2(s[t][2 + e] - ref);
-          l[t][e] = l[t][e] * al[t][e] + p[t][e] + p[t][2 + e];
+          // (compensated: nearly equal weights round the same way at every tile)
+          const float l0 = l[t][e] * al[t][e], x2 = fmaf(llost[t][e], al[t][e], p[t][e] + p[t][2 + e]);
+          l[t][e] = l0 + x2;
+          llost[t][e] = x2 - (l[t][e] - l0);
         }
       }
       if (__any_sync(0xffffffffu, moved)) {

@@ -14,8 +14,8 @@ Tolerances.  A row's channel is a sum of terms p D v.  Each term is off by
   - the exponentials (2 ulp each) and the products' parts: 8 x 2^-23.
 Those are taken as they stand.  The float32 sums over n tiles round to nearest,
 so their errors are as often up as down: an addition's is spread evenly over at
-most 2^-24 of the sum either way, so that their spread is 2^-24 sqrt(n/3) (and
-sqrt(2n/3) for the denominator, two additions a tile); 4 spreads are allowed.
+most 2^-24 of the sum either way, so that their spread is 2^-24 sqrt(n/3); 4
+spreads are allowed.  The denominator's sum is compensated and has 2^-23.
 All are relative to the sum of the terms' magnitudes (for y: through the norm or
 the denominator, which adds as much again)."""
 import math
@@ -84,7 +84,7 @@ def check(y, q, k, v, g, table, lens, w, norm, span, rows, eps=1e-6):
                 ref, bar = o * f * w.double(), (err * f + o.abs() * f * rel) * w.double().abs()
             else:
                 den = p.sum()
-                rel = float((p * logit).sum() / den) + 4 * math.sqrt(2 * span / 3) * 2 ** -24 + 8 * 2 ** -23
+                rel = float((p * logit).sum() / den) + 9 * 2 ** -23
                 ref, bar = o / den, err / den + o.abs() / den * rel
             bar = bar + ref.abs() * 2 ** -22
             got = y[b, h].double()
@@ -123,6 +123,27 @@ def test_steady_gates_over_many_tiles(cuda_lib, scalar, B, L, gate):
     args = make([L] * B, 1, 1, 16, 16, 64, scalar, lambda x: torch.full_like(x, -gate), torch.abs, 0.25,
                 1)
     both_norms(args, tiles, (0, B // 2, B - 1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scalar", [False, True])
+@pytest.mark.parametrize("top", [0.5, 8.0])
+def test_slowly_rising_logits(cuda_lib, scalar, top):
+    """Logits that rise evenly by `top` from the newest key to the oldest: the maximum moves at every tile, and all
+    weights of a tile are nearly equal, so that the sum of the weights rounds the same way for long."""
+    B, L, page = 1800, 32768, 64
+    q, k, *rest = args = make([L] * B, 1, 1, 16, 16, page, scalar, torch.zeros_like, torch.abs, seed=2)
+    rows = (0, B // 2, B - 1)
+    x = torch.arange(L, device="cuda").flip(0).double() / L * top
+    k[:, :, :, :2] = 0
+    for b in rows:                                          # as a sum of two bf16 channels, 16 bits
+        t = rest[2][b].long()
+        k[t] = 0
+        k[t, :, 0, 0] = x.to(bf16).view(-1, page)
+        k[t, :, 0, 1] = (x - x.to(bf16).double()).to(bf16).view(-1, page)
+    q.zero_()
+    q[:, :, :2] = 4.0                                       # and a scale of 1/4
+    both_norms(args, L // 16, rows)
 
 
 def line(lens, Hq, Hkv):
