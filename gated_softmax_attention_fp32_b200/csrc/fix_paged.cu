@@ -6,8 +6,8 @@
 // gate.
 //
 // Measured (B200, copy rate 6568 GB/s), Hq 32, Hkv 8, D 128, element-wise
-// gate: one sequence of 131,071 tokens in 170 to 174 us, 6.2 TB/s; 64 of 1 to
-// 8,191 in 103 to 106 us, 5.8 TB/s; one of 257 in 9.5 us.
+// gate: one sequence of 131,071 tokens in 170 to 175 us, 6.2 TB/s; 64 of 1 to
+// 8,191 in 104 to 110 us, 5.7 TB/s; one of 257 in 9.6 us.
 //
 // What bounds it: every cached byte is read once (1 KB per key and kv head at
 // D 128 with the element-wise gate), against 4 flops per q head and channel
@@ -36,6 +36,7 @@
 // Element-wise gate: V' = D v and P are fp32 values, split into two tf32
 // parts each (11 bits and more), three products: about 2^-21.  Scalar gate:
 // V stays bf16, D goes to P, which is split into three bf16 parts (24 bits).
+// Exponentials are ex2.approx, off by 2 ulp; below 2^-126 they are 0.
 // The tensor cores' own fp32 sums truncate, always towards zero, so that a sum
 // kept in them drifts (no gates, 32,768 keys in one warp: 2.8e-4 of y): they
 // add up one tile's products, from zero, and the running sums are added to
@@ -44,7 +45,11 @@
 // themselves, and the tile's sum is added to a compensated total (likewise
 // the pieces' totals in the join).  One running fp32 sum over all keys rounds
 // the same way at every step where the gates are steady (all of -1e-4, 32,768
-// keys in one warp: 9e-5 of y; now 1e-6).
+// keys in one warp: 9e-5 of y; now 1e-6).  The sum of the weights is
+// compensated for the same reason.  All this costs 4 to 6% where spans are
+// short (256 sequences of 90 to 900 tokens, 16 q heads per kv head: 51.4 ->
+// 53.3 us; 24 with the scalar gate, D 64: 20.4 -> 21.6) and 1% or nothing where the
+// memory sets the pace.
 #include <type_traits>
 
 #include "fix_internal.h"
