@@ -46,10 +46,11 @@
 // the pieces' totals in the join).  One running fp32 sum over all keys rounds
 // the same way at every step where the gates are steady (all of -1e-4, 32,768
 // keys in one warp: 9e-5 of y; now 1e-6).  The sum of the weights is
-// compensated for the same reason.  All this costs 4 to 6% where spans are
-// short (256 sequences of 90 to 900 tokens, 16 q heads per kv head: 51.4 ->
-// 53.3 us; 24 with the scalar gate, D 64: 20.4 -> 21.6) and 1% or nothing where the
-// memory sets the pace.
+// compensated for the same reason.  The values' running sums are not, for want
+// of registers: equal weights and equal values in 32,768 keys, no norm, 2e-5.
+// All this costs 4 to 6% where spans are short (256 sequences of 90 to 900
+// tokens, 16 q heads per kv head: 51.4 -> 53.3 us; 24 with the scalar gate,
+// D 64: 20.4 -> 21.6) and 1% or nothing where the memory sets the pace.
 #include <type_traits>
 
 #include "fix_internal.h"
